@@ -220,6 +220,201 @@ int qknorm_apply_with_stats(const qknorm_operand_t* q, const qknorm_operand_t* k
 int qknorm_headwise(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype,
                     float eps, int64_t head_dim, int64_t gamma_head_stride, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Headwise QK-Norm with the position rotation, its gradients, appending to a
+ * paged cache, and attention over a 4-bit cache.
+ *
+ * The rotation (rotary position embedding) turns each pair (a, b) of a head's
+ * first rot_dim columns by its position's angle: (a c - b s, b c + a s). The
+ * angles' cos and sin come from a table the caller keeps.
+ * ------------------------------------------------------------------------ */
+
+/* Widest head of the calls below (attention has its own widths). */
+#define QKNORM_MAX_ROPE_HEAD 1024
+
+/* Where the rotation's angles come from. */
+typedef struct qknorm_rope {
+  const float* cos_sin;      /* device float32 table [n_positions][rot_dim]: row p holds the cos of
+                                position p's rot_dim/2 angles, then their sin */
+  int64_t ld;                /* row stride in elements, >= rot_dim */
+  int64_t n_positions;       /* rows of the table, > 0 */
+  const int64_t* positions;  /* device int64 [T]: each token's position. One outside
+                                [0, n_positions) makes the token's rotated columns NaN. */
+  int64_t rot_dim;           /* even, in [0, head_dim]: columns of each head that are rotated.
+                                0: no rotation, the other fields are not used */
+  int interleaved;           /* 0: column i pairs with column i + rot_dim/2;
+                                1: column 2i pairs with column 2i + 1 */
+} qknorm_rope_t;
+
+/*
+ * qknorm_headwise_rope -- headwise QK-Norm (as qknorm_headwise), then the
+ * rotation of every head, in one pass: each element is read once and written
+ * once, rounded once after the rotation.
+ *
+ *   rope  the rotation (host pointer); NULL is the same as rot_dim = 0
+ *   other arguments as for qknorm_headwise. head_dim <= QKNORM_MAX_ROPE_HEAD.
+ *
+ * Outputs may be in place (y == x with ld_y == ld_x); the table and positions
+ * must not overlap the outputs.
+ */
+int qknorm_headwise_rope(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype,
+                         float eps, int64_t head_dim, int64_t gamma_head_stride,
+                         const qknorm_rope_t* rope, void* stream);
+
+/* One of Q or K of the backward pass. */
+typedef struct qknorm_grad_operand {
+  const void* x;     /* the forward call's input rows */
+  int64_t ld_x;      /* row strides in elements, >= h */
+  const void* dy;    /* gradient of the forward call's output, rows of the row type */
+  int64_t ld_dy;
+  void* dx;          /* out: gradient of x, rows of the row type. dx == dy or dx == x with the same
+                        stride is in place; any other overlap with an input or output is rejected. */
+  int64_t ld_dx;
+  const void* gamma; /* as in the forward call */
+  float* dgamma;     /* out: gradient of gamma, float32, laid out as gamma (overwritten, not added to;
+                        elements between heads of a stride > head_dim are left alone). NULL: not wanted */
+  int64_t h;
+} qknorm_grad_operand_t;
+
+/*
+ * qknorm_headwise_rope_backward -- gradients of qknorm_headwise_rope (and with
+ * rot_dim = 0 of qknorm_headwise): with g the gradient turned back by the
+ * rotation, r the head's factor, xr = x r and gg = g gamma,
+ *     dx = r (gg - xr mean(gg xr)),   dgamma_j = sum g_j xr_j
+ * over all tokens and over the heads that share gamma. Sums are in a fixed
+ * order: the same call gives the same bits.
+ *
+ *   dtype              QKNORM_F32 or QKNORM_BF16
+ *   gamma_head_stride  0 (shared) or >= head_dim
+ *   workspace          device memory of at least
+ *                      qknorm_headwise_rope_backward_workspace(...) bytes, 16-byte
+ *                      aligned, not shared with a call that may run at the same
+ *                      time; its contents need no preparation. May be NULL where
+ *                      that size is 0.
+ * T == 0 launches nothing, and dgamma is then not written.
+ */
+int qknorm_headwise_rope_backward(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T,
+                                  int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                                  const qknorm_rope_t* rope, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Bytes of workspace that a backward call of these sizes needs (0 for sizes
+ * it would reject; makes no HIP call). */
+size_t qknorm_headwise_rope_backward_workspace(int64_t hq, int64_t hk, int64_t T, int dtype, int64_t head_dim,
+                                               int64_t gamma_head_stride);
+
+typedef enum qknorm_cache_format {
+  QKNORM_CACHE_ROWS = 0,  /* elements of the row type */
+  QKNORM_CACHE_MXFP4 = 1  /* 4 bits an element: E2M1 codes (0 .5 1 1.5 2 3 4 6 and their negatives;
+                             an even channel in its byte's low half) and one E8M0 scale byte (2^(byte - 127))
+                             per 32 channels of a head. Written blocks take E = floor(log2(largest
+                             magnitude)) - 2, held to [-100, 125], codes rounded to nearest even and
+                             saturated at 6. A block that held an infinity or NaN gets the byte 255; bytes
+                             above 252 read as NaN. */
+} qknorm_cache_format_t;
+
+/*
+ * A paged cache of keys and values. Token `slot % page_size` of page `slot /
+ * page_size` and key head h begins at
+ *     k + page * page_stride + h * head_stride + token * token_stride
+ * (elements of the row type, or bytes for MXFP4), head_dim consecutive elements
+ * (head_dim / 2 bytes); its scales at
+ *     k_scales + page * scale_page_stride + h * scale_head_stride + token * head_dim / 32
+ * (bytes). v is laid out alike.
+ */
+typedef struct qknorm_cache {
+  int format;              /* qknorm_cache_format_t */
+  void* k;
+  void* v;
+  void* k_scales;          /* MXFP4 only, as are the two strides below */
+  void* v_scales;
+  int64_t page_stride;     /* MXFP4: multiples of 16, and k and v 16-byte aligned */
+  int64_t head_stride;
+  int64_t token_stride;    /* MXFP4: head_dim / 2 (a head's tokens are packed) */
+  int64_t scale_page_stride;   /* multiples of 16, and the scales 16-byte aligned */
+  int64_t scale_head_stride;
+  int64_t n_pages;         /* > 0 */
+  int64_t page_size;       /* tokens, a power of two; MXFP4: at least 16 */
+  int64_t heads;           /* key heads */
+} qknorm_cache_t;
+
+/*
+ * qknorm_paged_append -- a step's keys and values into a paged cache, and its
+ * queries made ready, in one pass over packed QKV rows: Q heads are
+ * normalized and rotated into q->y, K heads normalized and rotated into the
+ * cache, V heads taken as they are.
+ *
+ *   q      NULL: only K and V are appended. q->y as in qknorm_headwise_rope.
+ *   k, v   k->h == v->h == cache->heads * head_dim. k->y and v->y may be NULL;
+ *          otherwise they receive, as rows, the values the cache now holds.
+ *   gamma  q->gamma or k->gamma NULL: that side is rotated but not normalized
+ *          (for example after qknorm_fused). v->gamma is not used.
+ *   slots  device int64 [T]: where each token goes (page * page_size + place in
+ *          the page). A token whose slot is negative, or past the last page,
+ *          is passed over: nothing of its row is written anywhere. No two
+ *          tokens of a call may have the same slot (which of them, or which
+ *          mixture, is kept would be undefined).
+ *   dtype  QKNORM_F32 or QKNORM_BF16
+ *   other arguments as for qknorm_headwise_rope.
+ *
+ * MXFP4 needs head_dim % 32 == 0. Keys bound for 4 bits are formed in float64,
+ * so a code is what exact arithmetic gives. No other slot of the cache is
+ * written. Outputs and the cache must not overlap each other or the inputs
+ * (q->y == q->x in place apart); k->y and v->y may not be in place.
+ */
+int qknorm_paged_append(const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
+                        int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                        const qknorm_rope_t* rope, const qknorm_cache_t* cache, const int64_t* slots, void* stream);
+
+/* The batch that qknorm_paged_attend works on. All arrays are device memory. */
+typedef struct qknorm_batch {
+  const int32_t* block_table;  /* [B][table_pages]: page ids in sequence order; row stride ld_table.
+                                  An id outside [0, n_pages) among a sequence's tokens makes the rows
+                                  that see them NaN. */
+  int64_t ld_table;
+  int64_t table_pages;
+  const int32_t* seq_lens;     /* [B] cached tokens, those of this call's queries among them; held to
+                                  [0, table_pages * page_size] */
+  const int32_t* cu_q;         /* [B + 1] first query row of each sequence, increasing, the last one
+                                  at most T; NULL: one query row per sequence (T == B). Rows outside
+                                  every sequence are left as they were. */
+  int64_t B;                   /* sequences, >= 0 */
+  int64_t max_q;               /* most query rows and cached tokens of any sequence, as far as the */
+  int64_t max_len;             /* caller knows (> 0): they shape the launch; larger ones stay correct */
+} qknorm_batch_t;
+
+/*
+ * qknorm_paged_attend -- attention of T query rows over a paged MXFP4 cache:
+ * out = softmax(scale q k^T + mask) v for each query head; head j reads key
+ * head j / (query heads / key heads). Query i of the n of a sequence stands at
+ * position seq_len - n + i and sees tokens up to its own (causal) or all
+ * (causal == 0) of the sequence, and with window > 0 only tokens at positions
+ * > its own - window. A row that sees nothing (an empty sequence, a position
+ * below 0) is 0.
+ *
+ *   q          x, ld_x, y, ld_y (rows of q->h = query heads * head_dim); gamma is
+ *              not used. 16-byte aligned, strides multiples of 8. y may not overlap x.
+ *   dtype      QKNORM_BF16
+ *   cache      format QKNORM_CACHE_MXFP4; the query heads are a multiple of cache->heads
+ *   head_dim   64, 128 or 256
+ *   scale      finite, > 0 (1/sqrt(head_dim) usually)
+ *   workspace  at least qknorm_paged_attend_workspace(...) bytes, 16-byte aligned,
+ *              not shared with a call that may run at the same time; its contents
+ *              need no preparation. May be NULL where that size is 0.
+ *
+ * Scores, softmax statistics and sums are float32; probabilities are rounded
+ * to bf16 for the second product, the result once more. Infinities and NaN of
+ * cached tokens reach only the rows that see those tokens.
+ */
+int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const qknorm_cache_t* cache,
+                        int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that an attend call of these sizes needs (0 for sizes it
+ * would reject; makes no HIP call). */
+size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
+                                     int64_t max_q, int64_t max_len);
+
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* qknorm_last_error(void);
 

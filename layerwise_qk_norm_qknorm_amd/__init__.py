@@ -22,3 +22,14 @@ from .binding import (  # noqa: F401
     prepare_headwise,
     prepare_partial_stats,
 )
+from .operators import (  # noqa: F401
+    prepare_headwise_rope,
+    prepare_headwise_rope_backward,
+    prepare_paged_append,
+    prepare_paged_attend,
+    qknorm_headwise_rope,
+    qknorm_headwise_rope_backward,
+    qknorm_paged_append,
+    qknorm_paged_attend,
+    rope_table,
+)

@@ -26,7 +26,10 @@ QKNORM_ERR_HIP = 3
 OP_FUSED, OP_PARTIAL_STATS, OP_APPLY_WITH_STATS = 0, 1, 2
 ABI_VERSION = 3
 EXPORTS = ("qknorm_fused", "qknorm_partial_stats", "qknorm_apply_with_stats", "qknorm_headwise",
-           "qknorm_last_error", "qknorm_abi_version", "qknorm_describe_plan", "qknorm_describe_headwise_plan")
+           "qknorm_last_error", "qknorm_abi_version", "qknorm_describe_plan", "qknorm_describe_headwise_plan",
+           "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "qknorm_headwise_rope_backward_workspace",
+           "qknorm_paged_append", "qknorm_paged_attend", "qknorm_paged_attend_workspace")
+CACHE_ROWS, CACHE_MXFP4 = 0, 1
 
 
 _DTYPES = {"f32": (QKNORM_F32, 4), "bf16": (QKNORM_BF16, 2), "fp8": (QKNORM_FP8_E4M3, 1)}
@@ -50,6 +53,70 @@ class Operand(ctypes.Structure):
         ("ld_y", ctypes.c_int64),
         ("gamma", ctypes.c_void_p),
         ("h", ctypes.c_int64),
+    ]
+
+
+class Rope(ctypes.Structure):
+    """qknorm_rope_t."""
+
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("n_positions", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int64),
+        ("interleaved", ctypes.c_int),
+    ]
+
+
+class GradOperand(ctypes.Structure):
+    """qknorm_grad_operand_t."""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64),
+        ("dy", ctypes.c_void_p),
+        ("ld_dy", ctypes.c_int64),
+        ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64),
+        ("gamma", ctypes.c_void_p),
+        ("dgamma", ctypes.c_void_p),
+        ("h", ctypes.c_int64),
+    ]
+
+
+class Cache(ctypes.Structure):
+    """qknorm_cache_t."""
+
+    _fields_ = [
+        ("format", ctypes.c_int),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("scale_page_stride", ctypes.c_int64),
+        ("scale_head_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+    ]
+
+
+class Batch(ctypes.Structure):
+    """qknorm_batch_t."""
+
+    _fields_ = [
+        ("block_table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("table_pages", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("cu_q", ctypes.c_void_p),
+        ("B", ctypes.c_int64),
+        ("max_q", ctypes.c_int64),
+        ("max_len", ctypes.c_int64),
     ]
 
 
@@ -82,8 +149,20 @@ def load_library():
         lib.qknorm_headwise.argtypes = [P, P, i64, ci, fl, i64, i64, vp]
         lib.qknorm_describe_headwise_plan.argtypes = [P, P, i64, ci, i64, i64, ctypes.c_char_p, ctypes.c_size_t]
         for fn in ("qknorm_fused", "qknorm_partial_stats", "qknorm_apply_with_stats", "qknorm_headwise",
-                   "qknorm_describe_plan", "qknorm_describe_headwise_plan", "qknorm_abi_version"):
+                   "qknorm_describe_plan", "qknorm_describe_headwise_plan", "qknorm_abi_version",
+                   "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "qknorm_paged_append",
+                   "qknorm_paged_attend"):
             getattr(lib, fn).restype = ci
+        R, G, C, B, sz = (ctypes.POINTER(Rope), ctypes.POINTER(GradOperand), ctypes.POINTER(Cache),
+                          ctypes.POINTER(Batch), ctypes.c_size_t)
+        lib.qknorm_headwise_rope.argtypes = [P, P, i64, ci, fl, i64, i64, R, vp]
+        lib.qknorm_headwise_rope_backward.argtypes = [G, G, i64, ci, fl, i64, i64, R, vp, sz, vp]
+        lib.qknorm_headwise_rope_backward_workspace.argtypes = [i64, i64, i64, ci, i64, i64]
+        lib.qknorm_headwise_rope_backward_workspace.restype = sz
+        lib.qknorm_paged_append.argtypes = [P, P, P, i64, ci, fl, i64, i64, R, C, vp, vp]
+        lib.qknorm_paged_attend.argtypes = [P, i64, ci, C, i64, B, fl, ci, i64, vp, sz, vp]
+        lib.qknorm_paged_attend_workspace.argtypes = [i64] * 7
+        lib.qknorm_paged_attend_workspace.restype = sz
         lib.qknorm_last_error.restype = ctypes.c_char_p
         lib.qknorm_last_error.argtypes = []
         lib.qknorm_abi_version.argtypes = []

@@ -25,7 +25,7 @@ CEIL_LIB = os.path.join(PKG, "libstreamceil.so")
 CLOCKS_LIB = os.path.join(PKG, "libqknorm_clocks.so")
 CEIL_CLOCKS_LIB = os.path.join(PKG, "libstreamceil_clocks.so")
 
-SOURCES = ["qknorm_api.cpp", "qknorm_kernels.hip"]
+SOURCES = ["qknorm_api.cpp", "qknorm_ops_api.cpp", "qknorm_kernels.hip", "qknorm_rope.hip", "qknorm_attend.hip"]
 CEIL_SOURCES = ["stream_ceiling.hip"]
 ARCH = "gfx950"
 

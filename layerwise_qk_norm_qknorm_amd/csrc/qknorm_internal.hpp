@@ -170,6 +170,9 @@ inline bool gamma_in_registers(const Plan& p) {
          (p.mode == MODE_FUSED || p.mode == MODE_APPLY);
 }
 
+// Largest grid a launch uses (the QKNORM_MAX_GRID cap).
+int64_t grid_cap();
+
 // Launches the kernel for `plan` on `stream`. Returns 0 or a HIP error code,
 // with a message in *err.
 int launch(const Plan& plan, const RowArgs& args, void* stream, std::string* err);
