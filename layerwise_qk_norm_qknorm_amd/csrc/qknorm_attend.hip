@@ -50,11 +50,19 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr uint32_t kTopScale = 252;       // largest scale byte of a finite block; above it, NaN
+// A row's reference maximum follows its scores only when they pass it by 2^8:
+// float32 sums and bf16 probabilities keep their relative accuracy at any
+// scale, and the accumulator is hardly ever rescaled.
+constexpr float kSlack = 8.0f;
 
 struct Frag {
   uint32_t w[4];
   __device__ __forceinline__ bf16x8_t get() const { return __builtin_bit_cast(bf16x8_t, *this); }
 };
+
+__device__ __forceinline__ uint32_t over(uint32_t n, const Divisor& d) {   // n / d
+  return (uint32_t)((uint64_t)n * d.mul >> (31 + d.shift));
+}
 
 template <int SEL>
 __device__ __forceinline__ uint32_t widen_pair(uint32_t codes, float scale) {
@@ -69,83 +77,157 @@ __device__ __forceinline__ uint32_t widen_byte(uint32_t codes, float scale, int 
   }
 }
 
+// The larger of three; a NaN operand loses, as with fmaxf. (Through fmaxf the
+// compiler spends an instruction per operand on quieting NaNs first.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 __device__ __forceinline__ float row_max(float v) {   // over the four lanes that hold a row
   auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  v = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[1]));
   p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  return max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[1]));
+}
+
+// A sequence's query rows and cached length, held to what the arrays hold.
+struct Sequence {
+  int q0, nq, len;
+};
+__device__ __forceinline__ Sequence sequence(const AttendArgs& a, int b) {
+  Sequence s{b, 1, a.seq_lens[b]};
+  if (a.cu_q) {
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+    s.q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
+    s.nq = (q1 < s.q0 ? s.q0 : q1 > a.T ? a.T : q1) - s.q0;
+  }
+  s.len = s.len < 0 ? 0 : s.len > a.table_tokens ? a.table_tokens : s.len;
+  return s;
+}
+// Tokens [lo, hi) that query i of a sequence sees.
+__device__ __forceinline__ int see_hi(const AttendArgs& a, const Sequence& s, int i) {
+  const int pos = s.len - s.nq + i;
+  return pos < 0 ? 0 : a.causal ? pos + 1 : s.len;
+}
+__device__ __forceinline__ int see_lo(const AttendArgs& a, const Sequence& s, int i) {
+  const int lo = s.len - s.nq + i - a.window + 1;
+  return a.window && lo > 0 ? lo : 0;
+}
+// A block's rows r0 .. : what they see together, and the chunks that takes.
+struct Span {
+  int first, hi;     // first: a multiple of 32
+  int chunks;
+};
+__device__ __forceinline__ Span span(const AttendArgs& a, const Sequence& s, int i_first, int i_last) {
+  Span p;
+  const int lo = see_lo(a, s, i_first);
+  p.hi = see_hi(a, s, i_last);
+  p.first = lo & ~31;
+  p.chunks = p.hi > lo ? (int)((uint32_t)(p.hi - p.first + a.chunk - 1) / (uint32_t)a.chunk) : 0;
+  return p;
 }
 
 // Codes and scales of one 32-token tile, as one lane holds them: lane = 16 g
 // + m. K: token m of each half, a quarter of its channels (chosen by g). V:
 // tokens 4g .. 4g+3 of each half, channels m * D/16 and on.
 template <int D>
-struct Tile {
-  static constexpr int KW = D / 32;               // words of K codes per half
-  static constexpr int KS = D == 256 ? 2 : 1;     // K scales per half
-  static constexpr int VW = D == 256 ? 2 : 1;     // words of V codes per token
-  uint32_t k[2][KW];
-  uint32_t ks[2][KS];
-  uint32_t v[2][4][VW];
-  uint32_t vs[2][4];                              // V scale bytes
-  bool lost[2];                                   // the page id was out of range
+struct KTile {
+  static constexpr int W = D / 32;               // words of codes per half
+  static constexpr int S = D == 256 ? 2 : 1;     // scales per half
+  uint32_t c[2][W];
+  uint32_t s[2][S];
+};
+template <int D>
+struct VTile {
+  static constexpr int W = D == 256 ? 2 : 1;     // words of codes per token
+  uint32_t c[2][4][W];
+  uint32_t s[2][4];                              // the words that hold the scale bytes
 };
 
-template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& T, const AttendArgs& a, const int32_t* table, int64_t head_codes,
-                                          int64_t head_scales, int64_t tok, int64_t last16, int lane) {
-  const int m = lane & 15, g = lane >> 4;
+// Page ids of a tile's two halves (looked up a tile ahead of its loads, which
+// wait for them).
+struct Pages {
+  int id[2];
+};
+__device__ __forceinline__ Pages find_pages(const AttendArgs& a, const int32_t* table, int tok, int last16) {
+  Pages p;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     // past the end of the sequence: its last 16 tokens again, masked later
-    int64_t t = tok + 16 * h;
-    t = t < last16 ? t : last16;
-    int page = table[t >> a.log2_page];
-    T.lost[h] = page < 0 || page >= a.n_pages;
-    page = T.lost[h] ? 0 : page;
-    const int off = (int)(t & (((int64_t)1 << a.log2_page) - 1));
-    const int64_t c0 = page * a.page_stride + head_codes + (int64_t)off * (D / 2);
-    const int64_t s0 = page * a.scale_page_stride + head_scales + (int64_t)off * (D / 32);
-    const uint8_t* kc = a.cache[0] + c0;
-    const uint8_t* vc = a.cache[1] + c0;
-    const uint8_t* ks = a.scales[0] + s0;
-    const uint8_t* vs = a.scales[1] + s0;
+    const int t = min(tok + 16 * h, last16);
+    p.id[h] = table[t >> a.log2_page];
+  }
+  return p;
+}
+
+// Byte offsets of the codes and scales of a tile half's first token.
+struct Offsets {
+  int64_t codes, scales;
+};
+__device__ __forceinline__ Offsets offsets(const AttendArgs& a, int page_id, int tok, int half, int last16, int row_bytes) {
+  const int off = min(tok + 16 * half, last16) & ((1 << a.log2_page) - 1);
+  const int64_t page = (uint32_t)page_id < (uint64_t)a.n_pages ? page_id : 0;
+  return {page * a.page_stride + (int64_t)off * row_bytes, page * a.scale_page_stride + (int64_t)off * (row_bytes >> 4)};
+}
+
+template <int D>
+__device__ __forceinline__ void load_k(KTile<D>& T, const uint8_t* codes, const uint8_t* scales, const AttendArgs& a,
+                                       const Pages& pages, int tok, int last16, int lane) {
+  const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const Offsets o = offsets(a, pages.id[h], tok, h, last16, D / 2);
+    const uint8_t* c = codes + o.codes;
+    const uint8_t* s = scales + o.scales;
     if constexpr (D == 64) {
-      const u32x2_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(kc + m * 32 + g * 8));
-      T.k[h][0] = w.x, T.k[h][1] = w.y;
-      T.ks[h][0] = ks[m * 2 + (g >> 1)];
+      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(c + (uint32_t)(m * 32 + g * 8));
+      T.c[h][0] = w.x, T.c[h][1] = w.y;
+      T.s[h][0] = s[(uint32_t)(m * 2 + (g >> 1))];
     } else {
 #pragma unroll
       for (int sp = 0; sp < D / 128; ++sp) {
-        const u32x4_t w =
-            __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(kc + m * (D / 2) + 64 * sp + g * 16));
-        T.k[h][4 * sp] = w.x, T.k[h][4 * sp + 1] = w.y, T.k[h][4 * sp + 2] = w.z, T.k[h][4 * sp + 3] = w.w;
-        T.ks[h][sp] = ks[m * (D / 32) + 4 * sp + g];
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(c + (uint32_t)(m * (D / 2) + g * 16) + 64 * sp);
+        T.c[h][4 * sp] = w.x, T.c[h][4 * sp + 1] = w.y, T.c[h][4 * sp + 2] = w.z, T.c[h][4 * sp + 3] = w.w;
+        T.s[h][sp] = s[(uint32_t)(m * (D / 32) + g) + 4 * sp];
       }
     }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(VTile<D>& T, const uint8_t* codes, const uint8_t* scales, const AttendArgs& a,
+                                       const Pages& pages, int tok, int last16, int lane) {
+  const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const Offsets o = offsets(a, pages.id[h], tok, h, last16, D / 2);
+    const uint8_t* c = codes + o.codes;
+    const uint8_t* s = scales + o.scales;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint8_t* p = vc + (4 * g + j) * (D / 2) + m * (D / 32);
+      const uint8_t* p = c + (uint32_t)(4 * g * (D / 2) + m * (D / 32)) + j * (D / 2);
       if constexpr (D == 64) {
-        T.v[h][j][0] = *reinterpret_cast<const uint16_t*>(p);
+        T.c[h][j][0] = *reinterpret_cast<const uint16_t*>(p);
       } else if constexpr (D == 128) {
-        T.v[h][j][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+        T.c[h][j][0] = *reinterpret_cast<const uint32_t*>(p);
       } else {
-        const u32x2_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
-        T.v[h][j][0] = w.x, T.v[h][j][1] = w.y;
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+        T.c[h][j][0] = w.x, T.c[h][j][1] = w.y;
       }
     }
     // the scale words of the lane's four tokens; the byte is taken in use
     if constexpr (D == 64) {
-      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(vs + 8 * g);
-      T.vs[h][0] = w.x, T.vs[h][1] = w.x >> 16, T.vs[h][2] = w.y, T.vs[h][3] = w.y >> 16;
+      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(s + (uint32_t)(8 * g));
+      T.s[h][0] = w.x, T.s[h][1] = w.x >> 16, T.s[h][2] = w.y, T.s[h][3] = w.y >> 16;
     } else if constexpr (D == 128) {
-      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(vs + 16 * g);
-      T.vs[h][0] = w.x, T.vs[h][1] = w.y, T.vs[h][2] = w.z, T.vs[h][3] = w.w;
+      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(s + (uint32_t)(16 * g));
+      T.s[h][0] = w.x, T.s[h][1] = w.y, T.s[h][2] = w.z, T.s[h][3] = w.w;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        T.vs[h][j] = *reinterpret_cast<const uint32_t*>(vs + (4 * g + j) * 8 + (m >> 3) * 4);
+        T.s[h][j] = *reinterpret_cast<const uint32_t*>(s + (uint32_t)(32 * g + (m >> 3) * 4) + j * 8);
     }
   }
 }
@@ -157,234 +239,242 @@ __device__ __forceinline__ int k_channel(int g, int c) {
 }
 
 template <int D, int RT>
-__global__ void __launch_bounds__(64 * kWaves, RT * D <= 256 ? 2 : 1) qknorm_attend(const AttendArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 4 : RT * D <= 128 ? 3 : 2) qknorm_attend(const AttendArgs a) {
   constexpr int CB = D / 16;                 // 16-channel blocks of the output
   constexpr int LD = D + 4;                  // padded row of the join buffer
+  constexpr int KC = D / 32;                 // 8-channel chunks a lane holds of a row
+  constexpr bool QL = RT * D >= 256;         // queries in LDS, in fragment order, instead of registers
+  constexpr int NP = D == 256 ? 2 : 1;       // 32-channel blocks a lane's outputs lie in
+  // the join buffer; before the join, where QL, the queries
   __shared__ __align__(16) float red[kWaves * 16 * LD];
   __shared__ float red_m[kWaves * 16], red_l[kWaves * 16];
+  static_assert(!QL || RT * KC * 64 * sizeof(Frag) <= sizeof(red), "the queries fit the join buffer");
+  Frag* q_lds = reinterpret_cast<Frag*>(red);
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   // blocks of one (sequence, key head) lie a multiple of their count apart:
   // on one XCD, whose L2 then holds that head's cache, where it divides by 8
-  const uint32_t pairs = (uint32_t)a.B * a.heads_k;
-  const uint32_t rest = blockIdx.x / pairs;
-  const uint32_t pair = blockIdx.x - rest * pairs;
-  const int split = rest % (uint32_t)a.splits;
-  const int tile_of_grid = a.row_tiles - 1 - (int)(rest / (uint32_t)a.splits);   // long rows first
-  const int b = pair / (uint32_t)a.heads_k;
+  const uint32_t rest = over(blockIdx.x, a.by_pairs);
+  const uint32_t pair = blockIdx.x - rest * a.by_pairs.d;
+  const uint32_t tile_rev = over(rest, a.by_splits);
+  const int split = rest - tile_rev * a.by_splits.d;
+  const int grid_tile = a.row_tiles - 1 - (int)tile_rev;   // long rows first
+  const int b = over(pair, a.by_heads);
   const int hk = pair - b * a.heads_k;
 
-  int64_t q0 = b, nq = 1;
-  if (a.cu_q) {
-    q0 = a.cu_q[b];
-    int64_t q1 = a.cu_q[b + 1];
-    q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
-    q1 = q1 < q0 ? q0 : q1 > a.T ? a.T : q1;
-    nq = q1 - q0;
-  }
-  int64_t len = a.seq_lens[b];
-  len = len < 0 ? 0 : len > a.table_tokens ? a.table_tokens : len;
-  const int64_t last16 = len > 0 ? (len - 1) & ~(int64_t)15 : 0;
+  const Sequence seq = sequence(a, b);
+  const int last16 = seq.len > 0 ? (seq.len - 1) & ~15 : 0;
   const int32_t* table = a.table + b * a.ld_table;
-  const int64_t head_codes = hk * a.head_stride, head_scales = hk * a.scale_head_stride;
-  const int64_t rows = nq * a.group;
+  const uint8_t* kc = a.cache[0] + hk * a.head_stride;
+  const uint8_t* vc = a.cache[1] + hk * a.head_stride;
+  const uint8_t* ks = a.scales[0] + hk * a.scale_head_stride;
+  const uint8_t* vs = a.scales[1] + hk * a.scale_head_stride;
+  const int rows = seq.nq * a.group;
   const int heads_q = a.heads_k * a.group;
 
-  for (int64_t r0 = (int64_t)tile_of_grid * (16 * RT); r0 < rows; r0 += (int64_t)a.row_tiles * (16 * RT)) {
-    // what the tile's rows see: tokens [lo, hi), all of them within [lo_all, hi_all)
-    const int64_t i_first = r0 / a.group;
-    const int64_t r_end = rows < r0 + 16 * RT ? rows : r0 + 16 * RT;
-    const int64_t i_last = (r_end - 1) / a.group;
-    const int64_t base = len - nq;           // position of query i: base + i
-    const auto hi_of = [&](int64_t i) {
-      const int64_t pos = base + i;
-      return pos < 0 ? (int64_t)0 : a.causal ? pos + 1 : len;
-    };
-    const auto lo_of = [&](int64_t i) {
-      const int64_t lo = base + i - a.window + 1;
-      return a.window && lo > 0 ? lo : (int64_t)0;
-    };
-    const int64_t lo = lo_of(i_first), hi = hi_of(i_last);
-    const int64_t lo_all = lo_of(i_last), hi_all = hi_of(i_first);
-    const int64_t first = lo & ~(int64_t)31;           // tiles start at multiples of 32 tokens
-    const int64_t chunks = hi > lo ? (hi - first + a.chunk - 1) / a.chunk : 0;
-    const bool joined = chunks > 1 && a.splits > 1;    // partial results: qknorm_attend_join finishes
-    if (split > 0 && split >= chunks) continue;        // nothing of the cache left for this block
+  for (int r0 = grid_tile * (16 * RT); r0 < rows; r0 += a.row_tiles * (16 * RT)) {
+    const int i_first = over(r0, a.by_group);
+    const int i_last = over(min(rows, r0 + 16 * RT) - 1, a.by_group);
+    const Span sp = span(a, seq, i_first, i_last);
+    const int lo_all = see_lo(a, seq, i_last), hi_all = see_hi(a, seq, i_first);   // every row sees these
+    const bool joined = sp.chunks > 1 && a.splits > 1;   // partial results: qknorm_attend_join finishes
+    if (split > 0 && split >= sp.chunks) continue;       // nothing of the cache left for this block
 
-    // row state: this lane's row of each tile is m
-    int row_lo[RT], row_hi[RT];
-    Frag q[RT][D / 32];
+    // This lane's row of each tile is m. What it sees is needed at the edges
+    // alone and formed there.
+    const auto limits = [&](int rt, int* lo, int* hi) {
+      const int r = r0 + rt * 16 + m;
+      const int i = r < rows ? (int)over(r, a.by_group) : 0;
+      *lo = see_lo(a, seq, i);
+      *hi = r < rows ? see_hi(a, seq, i) : 0;
+    };
+    Frag q[QL ? 1 : RT][KC];
+    if constexpr (QL) __syncthreads();   // the last rows' readers are done
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int64_t r = r0 + rt * 16 + m;
+      const int r = r0 + rt * 16 + m;
       const bool on = r < rows;
-      const int64_t i = on ? r / a.group : 0;
-      row_lo[rt] = on ? (int)(lo_of(i) - first < 0 ? 0 : lo_of(i) - first) : 0;
-      row_hi[rt] = on ? (int)(hi_of(i) - first) : 0;
-      const int head = hk * a.group + (int)(on ? r - i * a.group : 0);
-      const char* p = static_cast<const char*>(a.q) + ((q0 + i) * a.ldq + (int64_t)head * D) * 2;
+      const int i = on ? (int)over(r, a.by_group) : 0;
+      const int head = hk * a.group + (on ? r - i * a.group : 0);
+      const char* p = static_cast<const char*>(a.q) + ((int64_t)(seq.q0 + i) * a.ldq + (int64_t)head * D) * 2;
+      if (QL && rt % kWaves != wave) continue;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < KC; ++c) {
         u32x4_t w = {0, 0, 0, 0};
         if (on) w = *reinterpret_cast<const u32x4_t*>(p + k_channel<D>(g, c) * 2);
-        q[rt][c].w[0] = w.x, q[rt][c].w[1] = w.y, q[rt][c].w[2] = w.z, q[rt][c].w[3] = w.w;
+        const Frag f = {{w.x, w.y, w.z, w.w}};
+        if constexpr (QL) {
+          q_lds[(rt * KC + c) * 64 + lane] = f;
+        } else {
+          q[rt][c] = f;
+        }
       }
     }
-    float run_m[RT], run_l[RT];
-    f32x4_t acc[RT][CB];
+    if constexpr (QL) __syncthreads();
+    float run_m[RT];
+    f32x4_t acc[RT][CB], acc_l[RT];       // acc_l: the sums of the probabilities, by the same products
+    uint32_t poison = 0;                  // (tile, block of channels) that NaN values reached
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       run_m[rt] = -__builtin_inff();
-      run_l[rt] = 0.0f;
+      acc_l[rt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) acc[rt][cb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    for (int64_t ch = split; ch < chunks; ch += a.splits) {
-      const int64_t begin = first + ch * a.chunk;
-      const int64_t end = begin + a.chunk < hi ? begin + a.chunk : hi;
-      Tile<D> next;
-      int64_t tok = begin + 32 * wave;
-      if (tok < end) load_tile<D>(next, a, table, head_codes, head_scales, tok, last16, lane);
-      for (; tok < end; tok += 32 * kWaves) {
-        Tile<D> T = next;
-        if (tok + 32 * kWaves < end)
-          load_tile<D>(next, a, table, head_codes, head_scales, tok + 32 * kWaves, last16, lane);
-
+    int q_at = lane;   // where this lane's query fragments lie in LDS
+    for (int ch = split; ch < sp.chunks; ch += a.splits) {
+      const int begin = sp.first + ch * a.chunk;
+      const int end = min(begin + a.chunk, sp.hi);
+      constexpr int kStep = 32 * kWaves;
+      int tok = begin + 32 * wave;
+      // Each part of a tile is loaded as soon as the registers of the one
+      // before it are free: K during the second product, V during the first
+      // of the next tile. Loads past the end read the last tokens again.
+      KTile<D> K;
+      VTile<D> V;
+      Pages pages, ahead;
+      if (tok < end) {
+        pages = find_pages(a, table, tok, last16);
+        ahead = find_pages(a, table, tok + kStep, last16);
+        load_k<D>(K, kc, ks, a, pages, tok, last16, lane);
+        load_v<D>(V, vc, vs, a, pages, tok, last16, lane);
+      }
+      for (; tok < end; tok += kStep) {
+        const bool lost[2] = {(uint32_t)pages.id[0] >= (uint64_t)a.n_pages,
+                              (uint32_t)pages.id[1] >= (uint64_t)a.n_pages};
         // scores, transposed: lane (m, g) gets tokens 16h + 4g + i of row m
         f32x4_t s[RT][2];
-        bool kbad = T.lost[0] || T.lost[1];
+        uint32_t top_ks = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int x = 0; x < Tile<D>::KS; ++x) kbad = kbad || T.ks[h][x] > kTopScale;
-        const bool any_kbad = __builtin_amdgcn_ballot_w64(kbad) != 0;
+          for (int x = 0; x < KTile<D>::S; ++x) top_ks = max(top_ks, K.s[h][x]);
+        const bool any_kbad = __builtin_amdgcn_ballot_w64(top_ks > kTopScale) != 0 || lost[0] || lost[1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          Frag kf[D / 32];
+          Frag kf[KC];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const float scale = __uint_as_float(T.ks[h][D == 256 ? c >> 2 : 0] << 23);
+          for (int c = 0; c < KC; ++c) {
+            const float scale = __uint_as_float(K.s[h][D == 256 ? c >> 2 : 0] << 23);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) kf[c].w[p] = widen_byte(T.k[h][c], scale, p);
+            for (int p = 0; p < 4; ++p) kf[c].w[p] = widen_byte(K.c[h][c], scale, p);
           }
           if (any_kbad) {   // a NaN block, or a page that does not exist
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c)
+            for (int c = 0; c < KC; ++c) {
+              const bool bad = lost[h] || K.s[h][D == 256 ? c >> 2 : 0] > kTopScale;
 #pragma unroll
-              for (int p = 0; p < 4; ++p)
-                kf[c].w[p] = T.lost[h] || T.ks[h][D == 256 ? c >> 2 : 0] > kTopScale ? 0x7FC07FC0u : kf[c].w[p];
+              for (int p = 0; p < 4; ++p) kf[c].w[p] = bad ? 0x7FC07FC0u : kf[c].w[p];
+            }
           }
+          // read again for every half: held across them they would take RT * D / 8 registers
+          if constexpr (QL) asm volatile("" : "+v"(q_at));
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             s[rt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-              s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[c].get(), q[rt][c].get(), s[rt][h], 0, 0, 0);
+            for (int c = 0; c < KC; ++c) {
+              const Frag qf = QL ? q_lds[(rt * KC + c) * 64 + q_at] : q[QL ? 0 : rt][c];
+              s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[c].get(), qf.get(), s[rt][h], 0, 0, 0);
+            }
           }
         }
+        pages = ahead;
+        load_k<D>(K, kc, ks, a, pages, tok + kStep, last16, lane);
         const bool edge = tok < lo_all || tok + 32 > hi_all;
-        const int rel = (int)(tok - first) + 4 * g;
+        if (edge) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            int lo, hi;
+            limits(rt, &lo, &hi);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int t = tok + 4 * g + 16 * (j >> 2) + (j & 3);
+              if (!(t >= lo && t < hi)) s[rt][j >> 2][j & 3] = -__builtin_inff();
+            }
+          }
+        }
         Frag pf[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           float f[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] = s[rt][j >> 2][j & 3];
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int t = rel + 16 * (j >> 2) + (j & 3);
-              f[j] = t >= row_lo[rt] && t < row_hi[rt] ? f[j] : -__builtin_inff();
-            }
-          }
-          float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(f[0], f[1]), __builtin_fmaxf(f[2], f[3])),
-                                      __builtin_fmaxf(__builtin_fmaxf(f[4], f[5]), __builtin_fmaxf(f[6], f[7])));
-          top = row_max(top) * a.scale_log2;
-          if (__builtin_amdgcn_ballot_w64(top > run_m[rt]) != 0) {
-            const float nm = __builtin_fmaxf(run_m[rt], top);
+          const float top =
+              row_max(max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), max3(f[6], f[7], f[7]))) * a.scale_log2;
+          if (__builtin_amdgcn_ballot_w64(top > run_m[rt] + kSlack) != 0) {
+            const float nm = max3(run_m[rt], top, top);
             // nothing seen yet: both are -inf, and there is nothing to rescale
             const float alpha = run_m[rt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(run_m[rt] - nm);
             run_m[rt] = nm;
-            run_l[rt] *= alpha;
+            acc_l[rt] *= alpha;
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) acc[rt][cb] *= alpha;
           }
           const float off = run_m[rt] == -__builtin_inff() ? 0.0f : run_m[rt];
-          float sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            f[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(f[j], a.scale_log2, -off));
-            sum += f[j];
-          }
-          run_l[rt] += sum;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const f32x2_t two = {f[2 * j], f[2 * j + 1]};
+            const f32x2_t two = {__builtin_amdgcn_exp2f(__builtin_fmaf(f[2 * j], a.scale_log2, -off)),
+                                 __builtin_amdgcn_exp2f(__builtin_fmaf(f[2 * j + 1], a.scale_log2, -off))};
             pf[rt].w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2_t));
           }
         }
 
         // V scales of the lane's eight tokens
-        float sc[2][4];
-        bool vbad = false;
+        const int shift = 8 * (D == 64 ? m >> 3 : D == 128 ? m >> 2 : (m >> 1) & 3);
+        uint32_t byte[8];
+        uint32_t top_vs = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int q8 = D == 64 ? m >> 3 : D == 128 ? m >> 2 : (m >> 1) & 3;
-            uint32_t byte = (T.vs[h][j] >> (8 * q8)) & 0xFFu;
-            // behind the end of the sequence lies whatever the page held
-            if (edge && tok + 16 * h + 4 * g + j >= len) byte = 0;
-            vbad = vbad || byte > kTopScale;
-            sc[h][j] = __uint_as_float(byte << 23);
-          }
-        if (__builtin_amdgcn_ballot_w64(vbad) != 0) {
+        for (int j = 0; j < 8; ++j) {
+          byte[j] = __builtin_amdgcn_ubfe(V.s[j >> 2][j & 3], shift, 8);
+          // behind the end of the sequence lies whatever the page held
+          if (edge && tok + 16 * (j >> 2) + 4 * g + (j & 3) >= seq.len) byte[j] = 0;
+          top_vs = max(top_vs, byte[j]);
+        }
+        if (__builtin_amdgcn_ballot_w64(top_vs > kTopScale) != 0) {
           // NaN blocks among the values. A masked probability is 0 and 0 * NaN
           // would reach rows that do not see the token, so such blocks enter
-          // the product as zeros, and NaN goes to the rows that see them.
+          // the product as zeros, and the rows that see them are marked.
+          // Lane 16 G + M holds token 16h + 4G + j, channels M * D/16 and on;
+          // the outputs of lane (m, g) lie in the channels of M = 4g .. 4g+3.
+          for (int rt = 0; rt < RT; ++rt) {
+            int lo, hi;
+            limits(rt, &lo, &hi);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const bool bad = sc[h][j] > __uint_as_float(kTopScale << 23) || sc[h][j] != sc[h][j];
-#pragma unroll
-              for (int x = 0; x < Tile<D>::VW; ++x) T.v[h][j][x] = bad ? 0u : T.v[h][j][x];
-              const uint64_t who = __builtin_amdgcn_ballot_w64(bad);
-              sc[h][j] = bad ? 1.0f : sc[h][j];
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t who = __builtin_amdgcn_ballot_w64(byte[j] > kTopScale);
               if (who == 0) continue;
-              // lane 16 G + M reports token 16h + 4G + j, channels M * D/16 and on
               for (int G = 0; G < 4; ++G) {
-                const int t = (int)(tok - first) + 16 * h + 4 * G + j;
+                const int t = tok + 16 * (j >> 2) + 4 * G + (j & 3);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                  const bool sees = t >= row_lo[rt] && t < row_hi[rt];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const bool hit = sees && (who >> (16 * G + 4 * g + i) & 1);
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) acc[rt][cb][i] = hit ? __builtin_nanf("") : acc[rt][cb][i];
-                  }
-                }
+                for (int x = 0; x < NP; ++x)
+                  if (t >= lo && t < hi && (who >> (16 * G + 4 * g + 2 * x) & 1)) poison |= 1u << (rt * NP + x);
               }
             }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const bool bad = byte[j] > kTopScale;
+            byte[j] = bad ? 127 : byte[j];
+#pragma unroll
+            for (int x = 0; x < VTile<D>::W; ++x) V.c[j >> 2][j & 3][x] = bad ? 0u : V.c[j >> 2][j & 3][x];
+          }
         }
 
-        // out += V^T P^T: two 16-channel blocks per byte of codes
+        // out += V^T P^T: two 16-channel blocks per byte of codes; sums: a row of ones for V^T
 #pragma unroll
         for (int p = 0; p < CB / 2; ++p) {
           Frag even, odd;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const uint32_t x = widen_byte(T.v[h][j][p >> 2], sc[h][j], p & 3);
-              const uint32_t y = widen_byte(T.v[h][j + 1][p >> 2], sc[h][j + 1], p & 3);
-              even.w[2 * h + j / 2] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-              odd.w[2 * h + j / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-            }
+          for (int j = 0; j < 8; j += 2) {
+            const uint32_t x = widen_byte(V.c[j >> 2][j & 3][p >> 2], __uint_as_float(byte[j] << 23), p & 3);
+            const uint32_t y = widen_byte(V.c[j >> 2][(j & 3) + 1][p >> 2], __uint_as_float(byte[j + 1] << 23), p & 3);
+            even.w[j / 2] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            odd.w[j / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+          }
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             acc[rt][2 * p] =
@@ -393,30 +483,38 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 256 ? 2 : 1) qknorm_att
                 __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd.get(), pf[rt].get(), acc[rt][2 * p + 1], 0, 0, 0);
           }
         }
+        const Frag ones = {{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}};
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          acc_l[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones.get(), pf[rt].get(), acc_l[rt], 0, 0, 0);
+        load_v<D>(V, vc, vs, a, pages, tok + kStep, last16, lane);
+        ahead = find_pages(a, table, tok + 2 * kStep, last16);
       }
     }
 
     // Join the four waves: one row tile at a time through LDS.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      run_l[rt] = swap_add32(swap_add16(run_l[rt]));
       __syncthreads();   // the buffer's last readers are done
       if (g == 0) {
         red_m[wave * 16 + m] = run_m[rt];
-        red_l[wave * 16 + m] = run_l[rt];
+        red_l[wave * 16 + m] = acc_l[rt][0];
       }
       // lane (m, g) holds row m, channels (4g + i) * D/16 + cb
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const bool nan = poison >> (rt * NP + (NP > 1 ? i >> 1 : 0)) & 1;
 #pragma unroll
         for (int cb = 0; cb < CB; cb += 4) {
-          const f32x4_t v = {acc[rt][cb][i], acc[rt][cb + 1][i], acc[rt][cb + 2][i], acc[rt][cb + 3][i]};
+          f32x4_t v = {acc[rt][cb][i], acc[rt][cb + 1][i], acc[rt][cb + 2][i], acc[rt][cb + 3][i]};
+          if (nan) v = f32x4_t{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
           *reinterpret_cast<f32x4_t*>(&red[(wave * 16 + m) * LD + (4 * g + i) * CB + cb]) = v;
         }
+      }
       __syncthreads();
       const int row = threadIdx.x >> 4;                 // 16 threads per row
       const int col = (threadIdx.x & 15) * (D / 16);    // D/16 channels each
-      const int64_t r = r0 + rt * 16 + row;
+      const int r = r0 + rt * 16 + row;
       float top = -__builtin_inff();
       float w[kWaves], l = 0.0f;
 #pragma unroll
@@ -436,21 +534,18 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 256 ? 2 : 1) qknorm_att
         for (int x = 0; x < kWaves; ++x) o[e] += w[x] * red[(x * 16 + row) * LD + col + e];
       }
       if (r < rows) {
-        const int64_t i = r / a.group;
-        const int head = hk * a.group + (int)(r - i * a.group);
+        const int i = over(r, a.by_group);
+        const int head = hk * a.group + (r - i * a.group);
         if (joined) {
-          const int64_t at = ((q0 + i) * heads_q + head) * a.splits + split;
+          const int64_t at = ((int64_t)(seq.q0 + i) * heads_q + head) * a.splits + split;
 #pragma unroll
           for (int e = 0; e < D / 16; e += 4)
             *reinterpret_cast<f32x4_t*>(a.part_o + at * D + col + e) = f32x4_t{o[e], o[e + 1], o[e + 2], o[e + 3]};
-          if ((threadIdx.x & 15) == 0) {
-            a.part_ml[at * 2] = top;
-            a.part_ml[at * 2 + 1] = l;
-          }
+          if ((threadIdx.x & 15) == 0) *reinterpret_cast<f32x2_t*>(a.part_ml + at * 2) = f32x2_t{top, l};
         } else {
-          const bool empty = hi_of(i) <= lo_of(i);      // a row that sees nothing is zero
-          const float inv = empty ? 0.0f : 1.0f / l;
-          char* p = static_cast<char*>(a.out) + ((q0 + i) * a.ldo + (int64_t)head * D + col) * 2;
+          const bool empty = see_hi(a, seq, i) <= see_lo(a, seq, i);      // a row that sees nothing is zero
+          const float inv = 1.0f / l;
+          char* p = static_cast<char*>(a.out) + ((int64_t)(seq.q0 + i) * a.ldo + (int64_t)head * D + col) * 2;
           uint32_t u[D / 32];
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) {
@@ -467,74 +562,71 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 256 ? 2 : 1) qknorm_att
         }
       }
     }
-    __syncthreads();
   }
 }
 
-// Joins the chunks of rows whose cache was split: a wave per (query, head),
-// D/64 channels per lane. The row's chunk count follows from the same
-// arithmetic as in qknorm_attend; rows written there already are left alone.
+// Joins the chunks of rows whose cache was split: a block per (query, head),
+// D/4 threads across the row's columns, the rest along the chunks. The row's
+// chunk count follows from the same arithmetic as in qknorm_attend; rows
+// finished there are left alone.
 template <int D>
-__global__ void __launch_bounds__(256) qknorm_attend_join(const AttendArgs a, int row_tile, int64_t max_q) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ void __launch_bounds__(256) qknorm_attend_join(const AttendArgs a, int row_tile, int max_q) {
+  constexpr int CT = D / 4;             // threads across
+  constexpr int NG = 256 / CT;          // chunk groups
+  __shared__ __align__(16) float red[NG * D];
+  __shared__ float red_m[NG], red_l[NG];
+  const int head = blockIdx.y;
+  const int b = blockIdx.x / (uint32_t)max_q;
+  const Sequence seq = sequence(a, b);
   const int heads_q = a.heads_k * a.group;
-  const int64_t per_seq = max_q * heads_q;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-  const int64_t b = unit / per_seq;
-  if (b >= a.B) return;
-  int64_t q0 = b, nq = 1;
-  if (a.cu_q) {
-    q0 = a.cu_q[b];
-    int64_t q1 = a.cu_q[b + 1];
-    q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
-    q1 = q1 < q0 ? q0 : q1 > a.T ? a.T : q1;
-    nq = q1 - q0;
-  }
-  int64_t len = a.seq_lens[b];
-  len = len < 0 ? 0 : len > a.table_tokens ? a.table_tokens : len;
-  const int64_t u0 = unit - b * per_seq;
-  const int head = (int)(u0 % heads_q);
-  for (int64_t i = u0 / heads_q; i < nq; i += max_q) {
-    const int64_t rows = nq * a.group;
-    const int64_t r0 = (i * a.group + head % a.group) / (16 * row_tile) * (16 * row_tile);
-    const int64_t r_end = rows < r0 + 16 * row_tile ? rows : r0 + 16 * row_tile;
-    const int64_t i_first = r0 / a.group, i_last = (r_end - 1) / a.group;
-    const int64_t base = len - nq;
-    const int64_t pos = base + i_last;
-    const int64_t hi = pos < 0 ? 0 : a.causal ? pos + 1 : len;
-    const int64_t wlo = base + i_first - a.window + 1;
-    const int64_t lo = a.window && wlo > 0 ? wlo : 0;
-    const int64_t chunks = hi > lo ? (hi - (lo & ~(int64_t)31) + a.chunk - 1) / a.chunk : 0;
-    if (chunks <= 1) continue;
-    const int n = (int)(chunks < a.splits ? chunks : a.splits);
-    const int64_t at = ((q0 + i) * heads_q + head) * a.splits;
+  const int grp = threadIdx.x / CT, col = (threadIdx.x & (CT - 1)) * 4;
+  for (int i = blockIdx.x - b * max_q; i < seq.nq; i += max_q) {
+    const int rows = seq.nq * a.group;
+    const int in_group = head - (int)over(head, a.by_group) * a.group;
+    const int r0 = (int)((uint32_t)(i * a.group + in_group) / (uint32_t)(16 * row_tile)) * (16 * row_tile);
+    const Span sp = span(a, seq, over(r0, a.by_group), over(min(rows, r0 + 16 * row_tile) - 1, a.by_group));
+    if (sp.chunks <= 1) continue;
+    const int n = min(sp.chunks, a.splits);
+    const int64_t at = ((int64_t)(seq.q0 + i) * heads_q + head) * a.splits;
     const float* ml = a.part_ml + at * 2;
+    const float* po = a.part_o + at * D + col;
     float top = -__builtin_inff();
-    for (int s = lane; s < n; s += 64) top = __builtin_fmaxf(top, ml[2 * s]);
-    for (int x = 1; x < 64; x <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x));
-    float l = 0.0f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    const float* po = a.part_o + at * D + lane * E;
+    for (int s = grp; s < n; s += NG) top = __builtin_fmaxf(top, ml[2 * s]);
+    float l = 0.0f;
+    f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
+    for (int s = grp; s < n; s += NG) {
       const float ms = ml[2 * s], ls = ml[2 * s + 1];
       const float w = ms == -__builtin_inff() ? (ls == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(ms - top);
       l += w * ls;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += w * po[(int64_t)s * D + e];
+      o += *reinterpret_cast<const f32x4_t*>(po + (int64_t)s * D) * w;
     }
-    const int64_t my_pos = base + i;
-    const int64_t my_hi = my_pos < 0 ? 0 : a.causal ? my_pos + 1 : len;
-    const int64_t my_lo0 = my_pos - a.window + 1;
-    const int64_t my_lo = a.window && my_lo0 > 0 ? my_lo0 : 0;
-    const bool empty = my_hi <= my_lo;
-    const float inv = 1.0f / l;
-    __bf16* p = static_cast<__bf16*>(a.out) + (q0 + i) * a.ldo + (int64_t)head * D + lane * E;
+    __syncthreads();
+    *reinterpret_cast<f32x4_t*>(&red[grp * D + col]) = o;
+    if (col == 0) red_m[grp] = top, red_l[grp] = l;
+    __syncthreads();
+    if (grp == 0) {
+      float all = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < E; ++e) p[e] = (__bf16)(empty ? 0.0f : o[e] * inv);
+      for (int x = 0; x < NG; ++x) all = __builtin_fmaxf(all, red_m[x]);
+      l = 0.0f;
+      o = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+        const float w = red_m[x] == -__builtin_inff() ? (red_l[x] == 0.0f ? 0.0f : 1.0f)
+                                                      : __builtin_amdgcn_exp2f(red_m[x] - all);
+        l += w * red_l[x];
+        o += *reinterpret_cast<const f32x4_t*>(&red[x * D + col]) * w;
+      }
+      const bool empty = see_hi(a, seq, i) <= see_lo(a, seq, i);
+      const float inv = 1.0f / l;
+      o = empty ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : o * inv;
+      const f32x2_t x = {o[0], o[1]}, y = {o[2], o[3]};
+      *reinterpret_cast<u32x2_t*>(static_cast<char*>(a.out) +
+                                  ((int64_t)(seq.q0 + i) * a.ldo + (int64_t)head * D + col) * 2) =
+          u32x2_t{__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t)),
+                  __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2_t))};
+    }
   }
 }
 
@@ -565,13 +657,12 @@ int launch_attend(const AttendPlan& p, const AttendArgs& args, void* stream, std
                                  static_cast<hipStream_t>(stream));
   if (e == hipSuccess && a.splits > 1) {
     int rt = p.row_tile;
-    int64_t mq = p.max_q;
+    int mq = (int)p.max_q;
     void* jargs[] = {&a, &rt, &mq};
-    const int64_t units = (int64_t)a.B * mq * a.heads_k * a.group;
     const void* join = p.head_dim == 64    ? reinterpret_cast<const void*>(qknorm_attend_join<64>)
                        : p.head_dim == 128 ? reinterpret_cast<const void*>(qknorm_attend_join<128>)
                                            : reinterpret_cast<const void*>(qknorm_attend_join<256>);
-    e = hipLaunchKernel(join, dim3((unsigned)((units + 3) / 4)), dim3(256), jargs, 0,
+    e = hipLaunchKernel(join, dim3((unsigned)(a.B * mq), (unsigned)(a.heads_k * a.group)), dim3(256), jargs, 0,
                         static_cast<hipStream_t>(stream));
   }
   if (e != hipSuccess) {

@@ -103,11 +103,25 @@ int64_t rope_grad_rows(const RopeGradArgs& a);
 int launch_rope_grad(int dtype, bool interleaved, const RopePlan& plan, const RopeGradArgs& args, void* stream,
                      std::string* err);
 
+// Unsigned division by a constant of the launch, for numerators below 2^31:
+// n / d = n * mul >> (31 + shift) with mul = ceil(2^(31 + shift) / d) and
+// shift = ceil(log2 d) (Granlund and Montgomery's round-up method).
+struct Divisor {
+  uint32_t mul = 0, shift = 0, d = 1;
+};
+inline Divisor divisor(uint32_t d) {
+  Divisor r;
+  r.d = d;
+  while (((uint64_t)1 << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)((((uint64_t)1 << (31 + r.shift)) + d - 1) / d);
+  return r;
+}
+
 struct AttendArgs {
   const void* q;         // [T][heads_q * head_dim] bf16
   void* out;
   int64_t ldq, ldo;
-  int64_t T;
+  int T;
   const uint8_t* cache[2];    // K, V codes
   const uint8_t* scales[2];
   int64_t page_stride, head_stride, scale_page_stride, scale_head_stride;   // bytes
@@ -116,16 +130,17 @@ struct AttendArgs {
   int heads_k, group;    // query heads per key head
   const int32_t* table;
   int64_t ld_table;
-  int64_t table_tokens;  // tokens a table row can name
+  int table_tokens;      // tokens a table row can name
   const int32_t* seq_lens;
   const int32_t* cu_q;   // NULL: one query per sequence
   int B;
   int causal;
-  int64_t window;        // 0: none
+  int window;            // 0: none
   float scale_log2;      // scale * log2(e)
+  Divisor by_group, by_pairs, by_splits, by_heads;   // pairs: B * heads_k
   int row_tiles;         // blocks along a sequence's rows (each loops over the rest)
   int splits;            // blocks along the cache
-  int chunk;             // cached tokens a block takes at a time, a multiple of 32
+  int chunk;             // cached tokens a block takes at a time, a multiple of 128
   float* part_o;         // [T][heads_q][splits][head_dim]
   float* part_ml;        // [T][heads_q][splits][2]: maximum (base 2), sum
 };

@@ -679,11 +679,14 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   if (!attend_sizes_ok(T, heads_q, cache->heads, head_dim, batch->B, max_q, max_len))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
   AttendPlan p = plan_attend(head_dim, cache->heads, heads_q / cache->heads, batch->B, max_q, max_len);
-  if ((int64_t)batch->B * cache->heads * p.row_tiles > ((int64_t)1 << 31) / 8 / p.splits)
+  if ((int64_t)batch->B * cache->heads * p.row_tiles > INT32_MAX / p.splits)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the launch exceeds the grid", fn);
   const size_t need = attend_workspace(p, T, heads_q);
   if (need && (!workspace || !multiple(workspace, 16) || workspace_bytes < need))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the workspace must be 16-byte aligned, at least %zu bytes", fn, need);
+
+  if (T > INT32_MAX / 2 / (heads_q / cache->heads))
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: T = %lld query rows are too many", fn, (long long)T);
 
   const Region y{(uintptr_t)q->y, q->ld_y, q->h, T, 2};
   const Region ws = bytes_of(workspace, (int64_t)need);
@@ -706,7 +709,7 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   a.out = q->y;
   a.ldq = q->ld_x;
   a.ldo = q->ld_y;
-  a.T = T;
+  a.T = (int)T;
   a.cache[0] = (const uint8_t*)cache->k;
   a.cache[1] = (const uint8_t*)cache->v;
   a.scales[0] = (const uint8_t*)cache->k_scales;
@@ -721,13 +724,17 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   a.group = (int)(heads_q / cache->heads);
   a.table = batch->block_table;
   a.ld_table = batch->ld_table;
-  a.table_tokens = capacity;
+  a.table_tokens = (int)capacity;
   a.seq_lens = batch->seq_lens;
   a.cu_q = batch->cu_q;
   a.B = (int)batch->B;
   a.causal = causal != 0;
-  a.window = window;
+  a.window = window < capacity + T ? (int)window : 0;   // wider than any position: no limit
   a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.by_group = divisor((uint32_t)a.group);
+  a.by_pairs = divisor((uint32_t)(batch->B * cache->heads));
+  a.by_splits = divisor((uint32_t)p.splits);
+  a.by_heads = divisor((uint32_t)cache->heads);
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
   a.chunk = p.chunk;
