@@ -22,14 +22,20 @@ from .binding import (  # noqa: F401
     prepare_headwise,
     prepare_partial_stats,
 )
-from .operators import (  # noqa: F401
-    prepare_headwise_rope,
-    prepare_headwise_rope_backward,
-    prepare_paged_append,
-    prepare_paged_attend,
-    qknorm_headwise_rope,
-    qknorm_headwise_rope_backward,
-    qknorm_paged_append,
-    qknorm_paged_attend,
-    rope_table,
-)
+
+_OPERATORS = ("prepare_headwise_rope", "prepare_headwise_rope_backward", "prepare_paged_append",
+              "prepare_paged_attend", "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "qknorm_paged_append",
+              "qknorm_paged_attend", "rope_table")
+
+
+def __getattr__(name):
+    # operators.py imports torch, which this package otherwise leaves to the first call
+    if name in _OPERATORS:
+        from . import operators
+        globals().update({n: getattr(operators, n) for n in _OPERATORS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_OPERATORS))
