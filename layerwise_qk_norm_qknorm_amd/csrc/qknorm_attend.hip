@@ -54,6 +54,9 @@ constexpr uint32_t kTopScale = 252;       // largest scale byte of a finite bloc
 // float32 sums and bf16 probabilities keep their relative accuracy at any
 // scale, and the accumulator is hardly ever rescaled.
 constexpr float kSlack = 8.0f;
+// The reference before any score: below every finite score there is, and so
+// that its differences stay finite.
+constexpr float kNothing = -1.7e38f;
 
 struct Frag {
   uint32_t w[4];
@@ -85,6 +88,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// In a branch that few tiles take: keeps the compiler from running it for all
+// of them as selects (the edge masks alone are 96 instructions of a tile).
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
 __device__ __forceinline__ float row_max(float v) {   // over the four lanes that hold a row
   auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   v = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[1]));
@@ -97,9 +104,9 @@ struct Sequence {
   int q0, nq, len;
 };
 __device__ __forceinline__ Sequence sequence(const AttendArgs& a, int b) {
-  Sequence s{b, 1, a.seq_lens[b]};
+  Sequence s{b, 1, load_uniform(a.seq_lens + b)};
   if (a.cu_q) {
-    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+    const int q0 = load_uniform(a.cu_q + b), q1 = load_uniform(a.cu_q + b + 1);
     s.q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
     s.nq = (q1 < s.q0 ? s.q0 : q1 > a.T ? a.T : q1) - s.q0;
   }
@@ -157,77 +164,110 @@ __device__ __forceinline__ Pages find_pages(const AttendArgs& a, const int32_t* 
   for (int h = 0; h < 2; ++h) {
     // past the end of the sequence: its last 16 tokens again, masked later
     const int t = min(tok + 16 * h, last16);
-    p.id[h] = table[t >> a.log2_page];
+    p.id[h] = load_uniform(table + (t >> a.log2_page));
   }
   return p;
 }
 
-// Byte offsets of the codes and scales of a tile half's first token.
-struct Offsets {
-  int64_t codes, scales;
+// Where a tile's halves lie: byte offsets of their first tokens' codes and
+// scales within a key head, in scalar registers (the compiler forms 64-bit
+// products on the vector unit even of uniform values, and every address that
+// follows would then be a vector pair of its own).
+struct Place {
+  uint64_t codes[2], scales[2];
+  bool lost[2];      // the page does not exist
 };
-__device__ __forceinline__ Offsets offsets(const AttendArgs& a, int page_id, int tok, int half, int last16, int row_bytes) {
-  const int off = min(tok + 16 * half, last16) & ((1 << a.log2_page) - 1);
-  const int64_t page = (uint32_t)page_id < (uint64_t)a.n_pages ? page_id : 0;
-  return {page * a.page_stride + (int64_t)off * row_bytes, page * a.scale_page_stride + (int64_t)off * (row_bytes >> 4)};
+template <int D>
+__device__ __forceinline__ Place place_of(const AttendArgs& a, const Pages& pages, int tok, int last16) {
+  Place p;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int off = min(tok + 16 * h, last16) & ((1 << a.log2_page) - 1);
+    p.lost[h] = (uint32_t)pages.id[h] >= a.n_pages;
+    const uint32_t page = p.lost[h] ? 0 : pages.id[h];
+    p.codes[h] = uniform64(page * (uint64_t)a.page_stride + (uint32_t)off * (uint64_t)(D / 2));
+    p.scales[h] = uniform64(page * (uint64_t)a.scale_page_stride + (uint32_t)off * (uint64_t)(D / 32));
+  }
+  return p;
+}
+
+// A lane's byte offsets into a tile half.
+struct LaneOffsets {
+  uint32_t kc, ks, vc, vs;
+};
+template <int D>
+__device__ __forceinline__ LaneOffsets lane_offsets(int lane) {
+  const uint32_t m = lane & 15, g = lane >> 4;
+  LaneOffsets o;
+  o.kc = m * (D / 2) + g * (D == 64 ? 8 : 16);
+  o.ks = m * (D / 32) + (D == 64 ? g >> 1 : g);
+  o.vc = 4 * g * (D / 2) + m * (D / 32);
+  o.vs = 4 * g * (D / 32) + (D == 256 ? (m >> 3) * 4 : 0);
+  return o;
+}
+
+// A global load at a scalar base, a lane's byte offset and a constant. Both
+// are hidden from the compiler where they are used: it would otherwise add
+// the lane's offset to the loop-invariant part of the base, or widen it to 64
+// bits, once for the whole loop, and hold a vector pair for each load.
+template <class T>
+__device__ __forceinline__ T load_at(uint64_t base, uint32_t offset, int constant) {
+  typedef const T __attribute__((address_space(1)))* gptr;
+  return *reinterpret_cast<gptr>((base + (uint64_t)offset) + constant);
+}
+__device__ __forceinline__ uint64_t pinned(uint64_t v) {
+  asm volatile("" : "+s"(v));
+  return v;
 }
 
 template <int D>
-__device__ __forceinline__ void load_k(KTile<D>& T, const uint8_t* codes, const uint8_t* scales, const AttendArgs& a,
-                                       const Pages& pages, int tok, int last16, int lane) {
-  const int m = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void load_k(KTile<D>& T, uint64_t codes, uint64_t scales, const Place& at, LaneOffsets& o) {
+  asm volatile("" : "+v"(o.kc), "+v"(o.ks));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const Offsets o = offsets(a, pages.id[h], tok, h, last16, D / 2);
-    const uint8_t* c = codes + o.codes;
-    const uint8_t* s = scales + o.scales;
+    const uint64_t c = pinned(codes + at.codes[h]), s = pinned(scales + at.scales[h]);
     if constexpr (D == 64) {
-      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(c + (uint32_t)(m * 32 + g * 8));
+      const u32x2_t w = load_at<u32x2_t>(c, o.kc, 0);
       T.c[h][0] = w.x, T.c[h][1] = w.y;
-      T.s[h][0] = s[(uint32_t)(m * 2 + (g >> 1))];
+      T.s[h][0] = load_at<uint8_t>(s, o.ks, 0);
     } else {
 #pragma unroll
       for (int sp = 0; sp < D / 128; ++sp) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(c + (uint32_t)(m * (D / 2) + g * 16) + 64 * sp);
+        const u32x4_t w = load_at<u32x4_t>(c, o.kc, 64 * sp);
         T.c[h][4 * sp] = w.x, T.c[h][4 * sp + 1] = w.y, T.c[h][4 * sp + 2] = w.z, T.c[h][4 * sp + 3] = w.w;
-        T.s[h][sp] = s[(uint32_t)(m * (D / 32) + g) + 4 * sp];
+        T.s[h][sp] = load_at<uint8_t>(s, o.ks, 4 * sp);
       }
     }
   }
 }
 
 template <int D>
-__device__ __forceinline__ void load_v(VTile<D>& T, const uint8_t* codes, const uint8_t* scales, const AttendArgs& a,
-                                       const Pages& pages, int tok, int last16, int lane) {
-  const int m = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void load_v(VTile<D>& T, uint64_t codes, uint64_t scales, const Place& at, LaneOffsets& o) {
+  asm volatile("" : "+v"(o.vc), "+v"(o.vs));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const Offsets o = offsets(a, pages.id[h], tok, h, last16, D / 2);
-    const uint8_t* c = codes + o.codes;
-    const uint8_t* s = scales + o.scales;
+    const uint64_t c = pinned(codes + at.codes[h]), s = pinned(scales + at.scales[h]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint8_t* p = c + (uint32_t)(4 * g * (D / 2) + m * (D / 32)) + j * (D / 2);
       if constexpr (D == 64) {
-        T.c[h][j][0] = *reinterpret_cast<const uint16_t*>(p);
+        T.c[h][j][0] = load_at<uint16_t>(c, o.vc, j * (D / 2));
       } else if constexpr (D == 128) {
-        T.c[h][j][0] = *reinterpret_cast<const uint32_t*>(p);
+        T.c[h][j][0] = load_at<uint32_t>(c, o.vc, j * (D / 2));
       } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+        const u32x2_t w = load_at<u32x2_t>(c, o.vc, j * (D / 2));
         T.c[h][j][0] = w.x, T.c[h][j][1] = w.y;
       }
     }
     // the scale words of the lane's four tokens; the byte is taken in use
     if constexpr (D == 64) {
-      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(s + (uint32_t)(8 * g));
+      const u32x2_t w = load_at<u32x2_t>(s, o.vs, 0);
       T.s[h][0] = w.x, T.s[h][1] = w.x >> 16, T.s[h][2] = w.y, T.s[h][3] = w.y >> 16;
     } else if constexpr (D == 128) {
-      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(s + (uint32_t)(16 * g));
+      const u32x4_t w = load_at<u32x4_t>(s, o.vs, 0);
       T.s[h][0] = w.x, T.s[h][1] = w.y, T.s[h][2] = w.z, T.s[h][3] = w.w;
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        T.s[h][j] = *reinterpret_cast<const uint32_t*>(s + (uint32_t)(32 * g + (m >> 3) * 4) + j * 8);
+      for (int j = 0; j < 4; ++j) T.s[h][j] = load_at<uint32_t>(s, o.vs, j * 8);
     }
   }
 }
@@ -239,12 +279,16 @@ __device__ __forceinline__ int k_channel(int g, int c) {
 }
 
 template <int D, int RT>
-__global__ void __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 4 : RT * D <= 128 ? 3 : 2) qknorm_attend(const AttendArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_attend(const AttendArgs a) {
   constexpr int CB = D / 16;                 // 16-channel blocks of the output
   constexpr int LD = D + 4;                  // padded row of the join buffer
   constexpr int KC = D / 32;                 // 8-channel chunks a lane holds of a row
   constexpr bool QL = RT * D >= 256;         // queries in LDS, in fragment order, instead of registers
   constexpr int NP = D == 256 ? 2 : 1;       // 32-channel blocks a lane's outputs lie in
+  constexpr bool LM = true;
+  constexpr int DEPTH = 1;
+  constexpr bool LATE = RT * D >= 512;   // tiles in flight beside the current one
+  constexpr int kStep = 32 * kWaves;
   // the join buffer; before the join, where QL, the queries
   __shared__ __align__(16) float red[kWaves * 16 * LD];
   __shared__ float red_m[kWaves * 16], red_l[kWaves * 16];
@@ -267,10 +311,11 @@ __global__ void __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 4 : RT * D 
   const Sequence seq = sequence(a, b);
   const int last16 = seq.len > 0 ? (seq.len - 1) & ~15 : 0;
   const int32_t* table = a.table + b * a.ld_table;
-  const uint8_t* kc = a.cache[0] + hk * a.head_stride;
-  const uint8_t* vc = a.cache[1] + hk * a.head_stride;
-  const uint8_t* ks = a.scales[0] + hk * a.scale_head_stride;
-  const uint8_t* vs = a.scales[1] + hk * a.scale_head_stride;
+  // of this key head
+  const uint64_t kc = uniform64((uint64_t)a.cache[0] + hk * a.head_stride);
+  const uint64_t vc = uniform64((uint64_t)a.cache[1] + hk * a.head_stride);
+  const uint64_t ks = uniform64((uint64_t)a.scales[0] + hk * a.scale_head_stride);
+  const uint64_t vs = uniform64((uint64_t)a.scales[1] + hk * a.scale_head_stride);
   const int rows = seq.nq * a.group;
   const int heads_q = a.heads_k * a.group;
 
@@ -313,192 +358,245 @@ __global__ void __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 4 : RT * D 
       }
     }
     if constexpr (QL) __syncthreads();
-    float run_m[RT];
-    f32x4_t acc[RT][CB], acc_l[RT];       // acc_l: the sums of the probabilities, by the same products
+    // The sums of the probabilities: by the same products with up to two row
+    // tiles; with four, registers are short and the lanes add their own.
+    float run_m[RT], run_l[RT];
+    f32x4_t acc[RT][CB], acc_l[LM ? RT : 1];
     uint32_t poison = 0;                  // (tile, block of channels) that NaN values reached
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      run_m[rt] = -__builtin_inff();
-      acc_l[rt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      run_m[rt] = kNothing;
+      run_l[rt] = 0.0f;
+      if (LM || rt == 0) acc_l[LM ? rt : 0] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) acc[rt][cb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
+    LaneOffsets offs = lane_offsets<D>(lane);
     int q_at = lane;   // where this lane's query fragments lie in LDS
-    for (int ch = split; ch < sp.chunks; ch += a.splits) {
-      const int begin = sp.first + ch * a.chunk;
-      const int end = min(begin + a.chunk, sp.hi);
-      constexpr int kStep = 32 * kWaves;
-      int tok = begin + 32 * wave;
-      // Each part of a tile is loaded as soon as the registers of the one
-      // before it are free: K during the second product, V during the first
-      // of the next tile. Loads past the end read the last tokens again.
-      KTile<D> K;
-      VTile<D> V;
-      Pages pages, ahead;
-      if (tok < end) {
-        pages = find_pages(a, table, tok, last16);
-        ahead = find_pages(a, table, tok + kStep, last16);
-        load_k<D>(K, kc, ks, a, pages, tok, last16, lane);
-        load_v<D>(V, vc, vs, a, pages, tok, last16, lane);
-      }
-      for (; tok < end; tok += kStep) {
-        const bool lost[2] = {(uint32_t)pages.id[0] >= (uint64_t)a.n_pages,
-                              (uint32_t)pages.id[1] >= (uint64_t)a.n_pages};
-        // scores, transposed: lane (m, g) gets tokens 16h + 4g + i of row m
-        f32x4_t s[RT][2];
-        uint32_t top_ks = 0;
+
+    // One 32-token tile. Each part of the tile DEPTH steps on is loaded as
+    // soon as the registers of this one's are free: K after the first product,
+    // V after the second. Loads past the end read the last tokens again.
+    const auto tile = [&](KTile<D>& K, VTile<D>& V, Place& at, Pages& ahead, int tok, int end) {
+      // scores, transposed: lane (m, g) gets tokens 16h + 4g + i of row m
+      f32x4_t s[RT][2];
+      uint32_t top_ks = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int x = 0; x < KTile<D>::S; ++x) top_ks = max(top_ks, K.s[h][x]);
-        const bool any_kbad = __builtin_amdgcn_ballot_w64(top_ks > kTopScale) != 0 || lost[0] || lost[1];
+        for (int x = 0; x < KTile<D>::S; ++x) top_ks = max(top_ks, K.s[h][x]);
+      const bool any_kbad = __builtin_amdgcn_ballot_w64(top_ks > kTopScale) != 0 || at.lost[0] || at.lost[1];
+      // KH halves at a time: with queries in LDS both, so that a fragment is read once for them
+      constexpr int KH = QL && RT * D <= 512 && D <= 128 ? 2 : 1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          Frag kf[KC];
+      for (int h0 = 0; h0 < 2; h0 += KH) {
+        Frag kf[KH][KC];
+#pragma unroll
+        for (int h = h0; h < h0 + KH; ++h) {
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const float scale = __uint_as_float(K.s[h][D == 256 ? c >> 2 : 0] << 23);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) kf[c].w[p] = widen_byte(K.c[h][c], scale, p);
+            for (int p = 0; p < 4; ++p) kf[h - h0][c].w[p] = widen_byte(K.c[h][c], scale, p);
           }
           if (any_kbad) {   // a NaN block, or a page that does not exist
+            keep_branch();
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-              const bool bad = lost[h] || K.s[h][D == 256 ? c >> 2 : 0] > kTopScale;
+              const bool bad = at.lost[h] || K.s[h][D == 256 ? c >> 2 : 0] > kTopScale;
 #pragma unroll
-              for (int p = 0; p < 4; ++p) kf[c].w[p] = bad ? 0x7FC07FC0u : kf[c].w[p];
-            }
-          }
-          // read again for every half: held across them they would take RT * D / 8 registers
-          if constexpr (QL) asm volatile("" : "+v"(q_at));
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            s[rt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-              const Frag qf = QL ? q_lds[(rt * KC + c) * 64 + q_at] : q[QL ? 0 : rt][c];
-              s[rt][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[c].get(), qf.get(), s[rt][h], 0, 0, 0);
+              for (int p = 0; p < 4; ++p) kf[h - h0][c].w[p] = bad ? 0x7FC07FC0u : kf[h - h0][c].w[p];
             }
           }
         }
-        pages = ahead;
-        load_k<D>(K, kc, ks, a, pages, tok + kStep, last16, lane);
-        const bool edge = tok < lo_all || tok + 32 > hi_all;
-        if (edge) {
+        // read again for every tile: held across them they would take RT * D / 8 registers
+        if constexpr (QL) asm volatile("" : "+v"(q_at));
+        constexpr int RB = KH == 2 ? 1 : RT;   // row tiles whose fragments are read together
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            int lo, hi;
-            limits(rt, &lo, &hi);
+        for (int r0t = 0; r0t < RT; r0t += RB)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int t = tok + 4 * g + 16 * (j >> 2) + (j & 3);
-              if (!(t >= lo && t < hi)) s[rt][j >> 2][j & 3] = -__builtin_inff();
-            }
+          for (int c = 0; c < KC; ++c) {
+            Frag qf[RB];
+#pragma unroll
+            for (int x = 0; x < RB; ++x) qf[x] = QL ? q_lds[((r0t + x) * KC + c) * 64 + q_at] : q[QL ? 0 : r0t + x][c];
+#pragma unroll
+            for (int x = 0; x < RB; ++x)
+#pragma unroll
+              for (int h = h0; h < h0 + KH; ++h) {
+                f32x4_t& d = s[r0t + x][h];
+                if (c == 0) d = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[h - h0][c].get(), qf[x].get(), d, 0, 0, 0);
+              }
           }
-        }
-        Frag pf[RT];
+      }
+      if constexpr (LATE) load_v<D>(V, vc, vs, at, offs);
+      at = place_of<D>(a, ahead, tok + DEPTH * kStep, last16);
+      load_k<D>(K, kc, ks, at, offs);
+      // after the reads of the queries: a wait for LDS counts scalar loads too, and waits for all
+      ahead = find_pages(a, table, tok + 2 * DEPTH * kStep, last16);
+      const bool edge = tok < lo_all || tok + 32 > min(hi_all, end);
+      if (edge) {
+        keep_branch();
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = s[rt][j >> 2][j & 3];
-          const float top =
-              row_max(max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), max3(f[6], f[7], f[7]))) * a.scale_log2;
-          if (__builtin_amdgcn_ballot_w64(top > run_m[rt] + kSlack) != 0) {
-            const float nm = max3(run_m[rt], top, top);
-            // nothing seen yet: both are -inf, and there is nothing to rescale
-            const float alpha = run_m[rt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(run_m[rt] - nm);
-            run_m[rt] = nm;
-            acc_l[rt] *= alpha;
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) acc[rt][cb] *= alpha;
-          }
-          const float off = run_m[rt] == -__builtin_inff() ? 0.0f : run_m[rt];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x2_t two = {__builtin_amdgcn_exp2f(__builtin_fmaf(f[2 * j], a.scale_log2, -off)),
-                                 __builtin_amdgcn_exp2f(__builtin_fmaf(f[2 * j + 1], a.scale_log2, -off))};
-            pf[rt].w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2_t));
-          }
-        }
-
-        // V scales of the lane's eight tokens
-        const int shift = 8 * (D == 64 ? m >> 3 : D == 128 ? m >> 2 : (m >> 1) & 3);
-        uint32_t byte[8];
-        uint32_t top_vs = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          byte[j] = __builtin_amdgcn_ubfe(V.s[j >> 2][j & 3], shift, 8);
-          // behind the end of the sequence lies whatever the page held
-          if (edge && tok + 16 * (j >> 2) + 4 * g + (j & 3) >= seq.len) byte[j] = 0;
-          top_vs = max(top_vs, byte[j]);
-        }
-        if (__builtin_amdgcn_ballot_w64(top_vs > kTopScale) != 0) {
-          // NaN blocks among the values. A masked probability is 0 and 0 * NaN
-          // would reach rows that do not see the token, so such blocks enter
-          // the product as zeros, and the rows that see them are marked.
-          // Lane 16 G + M holds token 16h + 4G + j, channels M * D/16 and on;
-          // the outputs of lane (m, g) lie in the channels of M = 4g .. 4g+3.
-          for (int rt = 0; rt < RT; ++rt) {
-            int lo, hi;
-            limits(rt, &lo, &hi);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint64_t who = __builtin_amdgcn_ballot_w64(byte[j] > kTopScale);
-              if (who == 0) continue;
-              for (int G = 0; G < 4; ++G) {
-                const int t = tok + 16 * (j >> 2) + 4 * G + (j & 3);
-#pragma unroll
-                for (int x = 0; x < NP; ++x)
-                  if (t >= lo && t < hi && (who >> (16 * G + 4 * g + 2 * x) & 1)) poison |= 1u << (rt * NP + x);
-              }
-            }
-          }
+          int lo, hi;
+          limits(rt, &lo, &hi);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const bool bad = byte[j] > kTopScale;
-            byte[j] = bad ? 127 : byte[j];
-#pragma unroll
-            for (int x = 0; x < VTile<D>::W; ++x) V.c[j >> 2][j & 3][x] = bad ? 0u : V.c[j >> 2][j & 3][x];
+            const int t = tok + 4 * g + 16 * (j >> 2) + (j & 3);
+            if (!(t >= lo && t < min(hi, end))) s[rt][j >> 2][j & 3] = -__builtin_inff();
           }
         }
+      }
+      Frag pf[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = s[rt][j >> 2][j & 3];
+        // the lane's own largest score decides; the row's, over its four lanes, is needed when it moves
+        const float top = max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), max3(f[6], f[7], f[7]));
+        if (__builtin_amdgcn_ballot_w64(__builtin_fmaf(top, a.scale_log2, -run_m[rt]) > kSlack) != 0) {
+          keep_branch();
+          const float nm = max3(run_m[rt], row_max(top) * a.scale_log2, run_m[rt]);
+          const float alpha = __builtin_amdgcn_exp2f(run_m[rt] - nm);
+          run_m[rt] = nm;
+          if constexpr (LM) acc_l[LM ? rt : 0] *= alpha;
+          run_l[rt] *= alpha;
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) acc[rt][cb] *= alpha;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(f[j], a.scale_log2, -run_m[rt]));
+          if (!LM) run_l[rt] += f[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x2_t two = {f[2 * j], f[2 * j + 1]};
+          pf[rt].w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2_t));
+        }
+      }
 
-        // out += V^T P^T: two 16-channel blocks per byte of codes; sums: a row of ones for V^T
+      // V scales of the lane's eight tokens
+      const int shift = 8 * (D == 64 ? m >> 3 : D == 128 ? m >> 2 : (m >> 1) & 3);
+      uint32_t byte[8];
+      uint32_t top_vs = 0;
 #pragma unroll
-        for (int p = 0; p < CB / 2; ++p) {
-          Frag even, odd;
+      for (int j = 0; j < 8; ++j) {
+        byte[j] = __builtin_amdgcn_ubfe(V.s[j >> 2][j & 3], shift, 8);
+        top_vs = max(top_vs, byte[j]);
+      }
+      if (tok + 32 > seq.len) {   // behind the end of the sequence lies whatever the page held
+        keep_branch();
+        top_vs = 0;
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const uint32_t x = widen_byte(V.c[j >> 2][j & 3][p >> 2], __uint_as_float(byte[j] << 23), p & 3);
-            const uint32_t y = widen_byte(V.c[j >> 2][(j & 3) + 1][p >> 2], __uint_as_float(byte[j + 1] << 23), p & 3);
-            even.w[j / 2] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-            odd.w[j / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-          }
+        for (int j = 0; j < 8; ++j) {
+          if (tok + 16 * (j >> 2) + 4 * g + (j & 3) >= seq.len) byte[j] = 0;
+          top_vs = max(top_vs, byte[j]);
+        }
+      }
+      if (__builtin_amdgcn_ballot_w64(top_vs > kTopScale) != 0) {
+        keep_branch();
+        // NaN blocks among the values. A masked probability is 0 and 0 * NaN
+        // would reach rows that do not see the token, so such blocks enter
+        // the product as zeros, and the rows that see them are marked.
+        // Lane 16 G + M holds token 16h + 4G + j, channels M * D/16 and on;
+        // the outputs of lane (m, g) lie in the channels of M = 4g .. 4g+3.
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            acc[rt][2 * p] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(even.get(), pf[rt].get(), acc[rt][2 * p], 0, 0, 0);
-            acc[rt][2 * p + 1] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd.get(), pf[rt].get(), acc[rt][2 * p + 1], 0, 0, 0);
+        for (int rt = 0; rt < RT; ++rt) {
+          int lo, hi;
+          limits(rt, &lo, &hi);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint64_t who = __builtin_amdgcn_ballot_w64(byte[j] > kTopScale);
+            if (who == 0) continue;
+            for (int G = 0; G < 4; ++G) {
+              const int t = tok + 16 * (j >> 2) + 4 * G + (j & 3);
+#pragma unroll
+              for (int x = 0; x < NP; ++x)
+                if (t >= lo && t < min(hi, end) && (who >> (16 * G + 4 * g + 2 * x) & 1)) poison |= 1u << (rt * NP + x);
+            }
           }
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool bad = byte[j] > kTopScale;
+          byte[j] = bad ? 127 : byte[j];
+#pragma unroll
+          for (int x = 0; x < VTile<D>::W; ++x) V.c[j >> 2][j & 3][x] = bad ? 0u : V.c[j >> 2][j & 3][x];
+        }
+      }
+
+      // out += V^T P^T: two 16-channel blocks per byte of codes
+#pragma unroll
+      for (int p = 0; p < CB / 2; ++p) {
+        Frag even, odd;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint32_t x = widen_byte(V.c[j >> 2][j & 3][p >> 2], __uint_as_float(byte[j] << 23), p & 3);
+          const uint32_t y = widen_byte(V.c[j >> 2][(j & 3) + 1][p >> 2], __uint_as_float(byte[j + 1] << 23), p & 3);
+          even.w[j / 2] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+          odd.w[j / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          acc[rt][2 * p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even.get(), pf[rt].get(), acc[rt][2 * p], 0, 0, 0);
+          acc[rt][2 * p + 1] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd.get(), pf[rt].get(), acc[rt][2 * p + 1], 0, 0, 0);
+        }
+      }
+      if constexpr (LM) {   // a row of ones for V^T: the probabilities' sums
         const Frag ones = {{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}};
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          acc_l[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones.get(), pf[rt].get(), acc_l[rt], 0, 0, 0);
-        load_v<D>(V, vc, vs, a, pages, tok + kStep, last16, lane);
-        ahead = find_pages(a, table, tok + 2 * kStep, last16);
+          acc_l[LM ? rt : 0] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones.get(), pf[rt].get(), acc_l[LM ? rt : 0], 0, 0, 0);
+      }
+      if (!LATE) load_v<D>(V, vc, vs, at, offs);
+    };
+
+    for (int ch = split; ch < sp.chunks; ch += a.splits) {
+      const int begin = sp.first + ch * a.chunk;
+      const int end = min(begin + a.chunk, sp.hi);
+      int tok = begin + 32 * wave;
+      if (tok >= end) continue;
+      KTile<D> K[DEPTH];
+      VTile<D> V[DEPTH];
+      Place at[DEPTH];
+      Pages ahead[DEPTH];
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i)
+        at[i] = place_of<D>(a, find_pages(a, table, tok + i * kStep, last16), tok + i * kStep, last16);
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i) {
+        ahead[i] = find_pages(a, table, tok + (DEPTH + i) * kStep, last16);
+        // in the order in which the loop issues and awaits them: its waits
+        // count the loads behind the one they are for, and hold for both
+        __builtin_amdgcn_sched_barrier(0);
+        load_k<D>(K[i], kc, ks, at[i], offs);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!LATE) load_v<D>(V[i], vc, vs, at[i], offs);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // every step works all DEPTH tiles; one past the end of the chunk is
+      // masked whole (a branch around it would make the waits for the loads
+      // hold for both ways, and so wait for all)
+      for (; tok < end; tok += DEPTH * kStep) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) tile(K[i], V[i], at[i], ahead[i], tok + i * kStep, end);
       }
     }
 
     // Join the four waves: one row tile at a time through LDS.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
+      const float sum = LM ? acc_l[LM ? rt : 0][0] : swap_add32(swap_add16(run_l[rt]));
       __syncthreads();   // the buffer's last readers are done
       if (g == 0) {
         red_m[wave * 16 + m] = run_m[rt];
-        red_l[wave * 16 + m] = acc_l[rt][0];
+        red_l[wave * 16 + m] = sum;
       }
       // lane (m, g) holds row m, channels (4g + i) * D/16 + cb
 #pragma unroll
@@ -515,15 +613,13 @@ __global__ void __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 4 : RT * D 
       const int row = threadIdx.x >> 4;                 // 16 threads per row
       const int col = (threadIdx.x & 15) * (D / 16);    // D/16 channels each
       const int r = r0 + rt * 16 + row;
-      float top = -__builtin_inff();
+      float top = kNothing;
       float w[kWaves], l = 0.0f;
 #pragma unroll
       for (int x = 0; x < kWaves; ++x) top = __builtin_fmaxf(top, red_m[x * 16 + row]);
 #pragma unroll
       for (int x = 0; x < kWaves; ++x) {
-        const float mx = red_m[x * 16 + row];
-        // a wave that saw only NaN scores has no maximum, but a NaN sum to pass on
-        w[x] = mx == -__builtin_inff() ? (red_l[x * 16 + row] == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(mx - top);
+        w[x] = __builtin_amdgcn_exp2f(red_m[x * 16 + row] - top);   // a NaN sum passes through any weight
         l += w[x] * red_l[x * 16 + row];
       }
       float o[D / 16];
@@ -590,14 +686,14 @@ __global__ void __launch_bounds__(256) qknorm_attend_join(const AttendArgs a, in
     const int64_t at = ((int64_t)(seq.q0 + i) * heads_q + head) * a.splits;
     const float* ml = a.part_ml + at * 2;
     const float* po = a.part_o + at * D + col;
-    float top = -__builtin_inff();
+    float top = kNothing;
     for (int s = grp; s < n; s += NG) top = __builtin_fmaxf(top, ml[2 * s]);
     float l = 0.0f;
     f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int s = grp; s < n; s += NG) {
       const float ms = ml[2 * s], ls = ml[2 * s + 1];
-      const float w = ms == -__builtin_inff() ? (ls == 0.0f ? 0.0f : 1.0f) : __builtin_amdgcn_exp2f(ms - top);
+      const float w = __builtin_amdgcn_exp2f(ms - top);
       l += w * ls;
       o += *reinterpret_cast<const f32x4_t*>(po + (int64_t)s * D) * w;
     }
@@ -606,15 +702,14 @@ __global__ void __launch_bounds__(256) qknorm_attend_join(const AttendArgs a, in
     if (col == 0) red_m[grp] = top, red_l[grp] = l;
     __syncthreads();
     if (grp == 0) {
-      float all = -__builtin_inff();
+      float all = kNothing;
 #pragma unroll
       for (int x = 0; x < NG; ++x) all = __builtin_fmaxf(all, red_m[x]);
       l = 0.0f;
       o = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int x = 0; x < NG; ++x) {
-        const float w = red_m[x] == -__builtin_inff() ? (red_l[x] == 0.0f ? 0.0f : 1.0f)
-                                                      : __builtin_amdgcn_exp2f(red_m[x] - all);
+        const float w = __builtin_amdgcn_exp2f(red_m[x] - all);
         l += w * red_l[x];
         o += *reinterpret_cast<const f32x4_t*>(&red[x * D + col]) * w;
       }

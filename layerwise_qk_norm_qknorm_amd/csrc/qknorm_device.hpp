@@ -378,6 +378,16 @@ __device__ __forceinline__ Chunk load_global16(uint64_t addr) {
   return c;
 }
 
+// One element that no kernel of the launch writes, at a wave-uniform address:
+// through the constant address space the compiler uses a scalar load. As a
+// vector load (what it emits where it cannot rule out a store to the same
+// place) its use would wait for every row load issued before it.
+template <class T>
+__device__ __forceinline__ T load_uniform(const T* p) {
+  typedef const T __attribute__((address_space(4)))* cptr;
+  return *reinterpret_cast<cptr>(reinterpret_cast<uintptr_t>(p));
+}
+
 // A block-uniform 64-bit value, held in scalar registers: lanes that select
 // between two such values then need no vector arithmetic to form them.
 __device__ __forceinline__ uint64_t uniform64(uint64_t v) {

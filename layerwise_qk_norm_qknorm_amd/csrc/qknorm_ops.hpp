@@ -125,7 +125,7 @@ struct AttendArgs {
   const uint8_t* cache[2];    // K, V codes
   const uint8_t* scales[2];
   int64_t page_stride, head_stride, scale_page_stride, scale_head_stride;   // bytes
-  int64_t n_pages;
+  uint32_t n_pages;      // at most 2^31 - 1: ids are int32
   int log2_page;
   int heads_k, group;    // query heads per key head
   const int32_t* table;

@@ -718,7 +718,7 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   a.head_stride = cache->head_stride;
   a.scale_page_stride = cache->scale_page_stride;
   a.scale_head_stride = cache->scale_head_stride;
-  a.n_pages = cache->n_pages;
+  a.n_pages = (uint32_t)(cache->n_pages < INT32_MAX ? cache->n_pages : INT32_MAX);
   a.log2_page = log2_of(cache->page_size);
   a.heads_k = (int)cache->heads;
   a.group = (int)(heads_q / cache->heads);

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_rows(const Rop
   for (int64_t t = (int64_t)blockIdx.x * a.tokens + tok; t < a.T; t += step) {
     int64_t place = 0;
     if constexpr (MODE != ROPE_FORWARD) {
-      place = a.slots[t];
+      place = load_uniform(a.slots + t);
       if (place < 0 || place >= a.n_tokens_held) continue;   // a row that holds no token
     }
     Piece<PB> xa[S][NP], xb[S][NP];
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_rows(const Rop
       }
     }
     Angles<VW, NP, INTER> turn;
-    if (a.rot_pairs) turn.load(a.cos_sin, a.ld_table, a.n_positions, a.positions[t], a.rot >> 1, at);
+    if (a.rot_pairs) turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
 
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
       load_bytes<PB, true>(yr + oa[k], in.ya[k].w);
       load_bytes<PB, true>(yr + ob[k], in.yb[k].w);
     }
-    if (a.rot_pairs) in.turn.load(a.cos_sin, a.ld_table, a.n_positions, a.positions[t], a.rot >> 1, at);
+    if (a.rot_pairs) in.turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
   };
 
   const int64_t step = (int64_t)a.workers * kGradWaves;
