@@ -357,8 +357,9 @@ typedef struct qknorm_cache {
  *   dtype  QKNORM_F32 or QKNORM_BF16
  *   other arguments as for qknorm_headwise_rope.
  *
- * MXFP4 needs head_dim % 32 == 0. Keys bound for 4 bits are formed in float64,
- * so a code is what exact arithmetic gives. No other slot of the cache is
+ * MXFP4 needs head_dim % 32 == 0. Keys bound for 4 bits are formed in float32,
+ * and again in float64 where a code or a scale is near a border, so that the
+ * codes are what exact arithmetic gives. No other slot of the cache is
  * written. Outputs and the cache must not overlap each other or the inputs
  * (q->y == q->x in place apart); k->y and v->y may not be in place.
  */

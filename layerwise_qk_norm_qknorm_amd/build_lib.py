@@ -27,7 +27,8 @@ CEIL_LIB = os.path.join(PKG, "libstreamceil.so")
 CLOCKS_LIB = os.path.join(PKG, "libqknorm_clocks.so")
 CEIL_CLOCKS_LIB = os.path.join(PKG, "libstreamceil_clocks.so")
 
-SOURCES = ["qknorm_api.cpp", "qknorm_ops_api.cpp", "qknorm_kernels.hip", "qknorm_rope.hip", "qknorm_attend.hip"]
+SOURCES = ["qknorm_api.cpp", "qknorm_ops_api.cpp", "qknorm_kernels.hip", "qknorm_rope.hip",
+           "qknorm_rope_paired.hip", "qknorm_attend.hip"]
 CEIL_SOURCES = ["stream_ceiling.hip"]
 TORCH_LIB = os.path.join(PKG, "_qknorm_torch.so")
 TORCH_SOURCE = os.path.join(CSRC, "qknorm_torch.cpp")

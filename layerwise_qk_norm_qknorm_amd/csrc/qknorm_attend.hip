@@ -63,10 +63,6 @@ struct Frag {
   __device__ __forceinline__ bf16x8_t get() const { return __builtin_bit_cast(bf16x8_t, *this); }
 };
 
-__device__ __forceinline__ uint32_t over(uint32_t n, const Divisor& d) {   // n / d
-  return (uint32_t)((uint64_t)n * d.mul >> (31 + d.shift));
-}
-
 template <int SEL>
 __device__ __forceinline__ uint32_t widen_pair(uint32_t codes, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, SEL));

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "qknorm_internal.hpp"
+#include "qknorm_ops.hpp"
 
 namespace qkn {
 namespace {
@@ -376,6 +377,10 @@ __device__ __forceinline__ Chunk load_global16(uint64_t addr) {
   c.w[2] = v.z;
   c.w[3] = v.w;
   return c;
+}
+
+__device__ __forceinline__ uint32_t over(uint32_t n, const Divisor& d) {   // n / d
+  return (uint32_t)((uint64_t)n * d.mul >> (31 + d.shift));
 }
 
 // One element that no kernel of the launch writes, at a wave-uniform address:

@@ -10,6 +10,20 @@
 
 namespace qkn {
 
+// Unsigned division by a constant of the launch, for numerators below 2^31:
+// n / d = n * mul >> (31 + shift) with mul = ceil(2^(31 + shift) / d) and
+// shift = ceil(log2 d) (Granlund and Montgomery's round-up method).
+struct Divisor {
+  uint32_t mul = 0, shift = 0, d = 1;
+};
+inline Divisor divisor(uint32_t d) {
+  Divisor r;
+  r.d = d;
+  while (((uint64_t)1 << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)((((uint64_t)1 << (31 + r.shift)) + d - 1) / d);
+  return r;
+}
+
 // Widest head of the rotation kernels (columns).
 constexpr int kRopeMaxHead = 1024;
 
@@ -19,6 +33,8 @@ constexpr int kRopeMaxHead = 1024;
 // (16 or 8 bytes of the row type, or one element); pair p of a head is held
 // by lane p mod `lanes` of the head's group.
 struct RopePlan {
+  int whole = 0;        // 1: one 16-byte chunk of a head per lane (qknorm_rope.hip); the fields up to
+                        // `pairs` describe the other layout (qknorm_rope_paired.hip)
   int piece_bytes = 0;  // 16, 8 or the element size
   int vw = 1;           // elements per piece
   int pairs = 0;        // pairs per head
@@ -27,6 +43,8 @@ struct RopePlan {
   int slots = 1;        // wave passes (64 / lanes heads each) per wave
   int waves = 1;        // waves per token in one block
   int tokens = 1;       // tokens per block
+  int groups = 1;       // one chunk per lane: waves per token
+  int apart = 0;        // 1 (MXFP4): a launch for Q and one for K and V
 };
 
 struct RopeSide {  // one of Q, K, V
@@ -39,15 +57,20 @@ struct RopeSide {  // one of Q, K, V
 
 struct RopeArgs {
   RopeSide side[3];
-  int first[3];        // slot where each side begins (a slot holds heads of one side)
+  int first[3];        // slot (one chunk per lane: wave) where each side begins; neither mixes sides
   int n_slots;         // slots of a token
   int64_t T;
   int64_t gstride;
   int head_dim;
   int pairs, rot_pairs, rot;
   int log2_lanes;
+  int half_lanes;      // one chunk per lane, half-split: lanes between the members of a pair
+  int idle;            // 1: a head leaves some lanes or a side of a pair empty
   int waves, tokens;   // of a block: waves per token, tokens
   uint32_t waves_inv;  // 65536 / waves, rounded up
+  // one chunk per lane: waves per token, waves of the launch; `tokens` is then the tokens these cover
+  Divisor by_groups;
+  uint32_t units;
   const float* cos_sin;
   int64_t ld_table, n_positions;
   const int64_t* positions;
@@ -62,6 +85,9 @@ struct RopeArgs {
   int64_t scale_page_stride, scale_head_stride;     // bytes
   int y_wide;              // 1: the rows for cached values take 16-byte stores
 };
+
+constexpr int kRopeMaxWaves = 8;   // of a block, paired layout
+constexpr int kRopeWaves = 4;      // of a block, one chunk per lane
 
 enum RopeMode : int { ROPE_FORWARD = 0, ROPE_APPEND_ROWS = 1, ROPE_APPEND_MXFP4 = 2 };
 
@@ -87,6 +113,8 @@ struct RopeGradArgs {
   int head_dim;
   int pairs, rot_pairs, rot;
   int log2_lanes;
+  int half_lanes;
+  int idle;
   int workers;         // token workers (blocks) per slot
   const float* cos_sin;
   int64_t ld_table, n_positions;
@@ -95,27 +123,17 @@ struct RopeGradArgs {
   float* partial;      // [rows][head_dim], see rope_grad_rows
 };
 
-constexpr int kGradWaves = 8;   // waves of a gradient block, each with tokens of its own
+constexpr int kGradWaves = 4;   // waves of a gradient block, each with tokens of its own
+
+// The kernel of the paired layout for a plan (NULL: none).
+const void* rope_paired_kernel(int mode, int dtype, bool interleaved, const RopePlan& plan);
+const void* rope_paired_grad_kernel(int dtype, bool interleaved, const RopePlan& plan);
 
 // Rows of partial gamma gradients a launch writes.
 int64_t rope_grad_rows(const RopeGradArgs& a);
 
 int launch_rope_grad(int dtype, bool interleaved, const RopePlan& plan, const RopeGradArgs& args, void* stream,
                      std::string* err);
-
-// Unsigned division by a constant of the launch, for numerators below 2^31:
-// n / d = n * mul >> (31 + shift) with mul = ceil(2^(31 + shift) / d) and
-// shift = ceil(log2 d) (Granlund and Montgomery's round-up method).
-struct Divisor {
-  uint32_t mul = 0, shift = 0, d = 1;
-};
-inline Divisor divisor(uint32_t d) {
-  Divisor r;
-  r.d = d;
-  while (((uint64_t)1 << r.shift) < d) ++r.shift;
-  r.mul = (uint32_t)((((uint64_t)1 << (31 + r.shift)) + d - 1) / d);
-  return r;
-}
 
 struct AttendArgs {
   const void* q;         // [T][heads_q * head_dim] bf16

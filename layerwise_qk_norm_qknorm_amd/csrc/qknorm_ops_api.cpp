@@ -86,19 +86,31 @@ int check_rows(const char* fn, const char* what, const void* p, int64_t ld, int6
   return QKNORM_OK;
 }
 
-// The widest piece (16 bytes, 8 bytes, one element) that the head's shape and
-// every address allow, and the layout that follows. `aligned(piece bytes)`
-// answers for the addresses.
+// One 16-byte chunk of a head per lane, where chunks of the head and of half
+// the rotation are powers of two; else the widest piece (16 bytes, 8 bytes, one
+// element) that the shape allows. `aligned(bytes, angles)` answers for the
+// addresses: rows at multiples of `bytes`, the table at those of `angles`
+// elements.
 template <class F>
 RopePlan plan_pieces(int dtype, int64_t head_dim, int64_t rot, bool inter, F aligned) {
   RopePlan p;
   const int esz = row_elem_bytes(dtype);
+  const int full = 16 / esz;
+  if (head_dim % full == 0 && power_of_two(head_dim / full) && head_dim / full <= 64 &&
+      (inter ? rot % full == 0 : rot == 0 || ((rot / 2) % full == 0 && power_of_two(rot / 2 / full))) &&
+      aligned(16, inter ? full / 2 : full)) {
+    p.whole = 1;
+    p.piece_bytes = 16;
+    p.vw = full;
+    p.pairs = p.lanes = (int)(head_dim / full);
+    return p;
+  }
   for (int pb : {16, 8, esz}) {
     const int vw = pb / esz;
     if (vw > 1) {
       if (head_dim % (2 * vw) || (head_dim - rot) % (2 * vw) || rot % (2 * vw) || head_dim / (2 * vw) > 64) continue;
       if (!inter && (rot / 2) % vw) continue;
-      if (!aligned(pb)) continue;
+      if (!aligned(pb, vw)) continue;
     }
     p.piece_bytes = pb;
     p.vw = vw;
@@ -113,20 +125,27 @@ RopePlan plan_pieces(int dtype, int64_t head_dim, int64_t rot, bool inter, F ali
 
 int slots_of(int64_t heads, const RopePlan& p) { return (int)((heads * p.lanes + 63) / 64); }
 
-// Slots per wave, waves and tokens per block.
-void plan_waves(RopePlan* p, int n_slots, int64_t T) {
+// Slots per wave. Several share the token's angles and keep more loads in
+// flight; calls of few tokens spread their slots over more waves. The waves of
+// a side take whole numbers of slots, so of the counts tried the one that
+// leaves fewest idle, of equals the largest (10 + 2 heads of 128, 16384
+// tokens: four slots 24.1 us, two 26.3).
+void plan_waves(RopePlan* p, const int (&slots)[3], int64_t T) {
+  const int n = slots[0] + slots[1] + slots[2];
+  const auto groups = [&](int s) { return (slots[0] + s - 1) / s + (slots[1] + s - 1) / s + (slots[2] + s - 1) / s; };
   p->slots = 1;
-  if (p->piece_bytes == 16 && T * n_slots >= 4096) {
-    // several slots per wave share the token's angles and keep more loads in
-    // flight; the count that leaves the fewest slots idle, larger ones first
-    int best = n_slots;   // wasted slots
-    for (int s : {3, 2, 4}) {
-      const int waste = (n_slots + s - 1) / s * s - n_slots;
-      if (waste < best) best = waste, p->slots = s;
+  if (p->whole) {
+    if (T * n >= 8192) {
+      int best = n;
+      for (int s : {4, 3, 2})
+        if (groups(s) * s - n < best) best = groups(s) * s - n, p->slots = s;
     }
+    p->groups = groups(p->slots);
+    return;
   }
-  p->waves = (n_slots + p->slots - 1) / p->slots;
-  if (p->waves > 8) p->waves = 8;
+  if (p->piece_bytes == 16 && T * n >= 4096) p->slots = 3;
+  p->waves = (n + p->slots - 1) / p->slots;
+  if (p->waves > kRopeMaxWaves) p->waves = kRopeMaxWaves;
   p->tokens = p->waves >= 4 ? 1 : 4 / p->waves;
 }
 
@@ -140,9 +159,9 @@ void table_args(const qknorm_rope_t* rope, const RopePlan& p, int* rot, int* rot
   *pos = *rot ? rope->positions : nullptr;
 }
 
-bool table_aligned(const qknorm_rope_t* rope, int vw) {
+bool table_aligned(const qknorm_rope_t* rope, int angles) {
   if (!rope || !rope->rot_dim) return true;
-  const int64_t n = vw * 4 < 16 ? vw * 4 : 16;
+  const int64_t n = angles * 4 < 16 ? angles * 4 : 16;
   return multiple(rope->cos_sin, n) && rope->ld * 4 % n == 0 && rope->rot_dim / 2 * 4 % n == 0;
 }
 
@@ -328,14 +347,14 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
 
   const int64_t rot = rope ? rope->rot_dim : 0;
   const bool inter = rot && rope->interleaved;
-  out->plan = plan_pieces(dtype, head_dim, rot, inter, [&](int pb) {
+  out->plan = plan_pieces(dtype, head_dim, rot, inter, [&](int pb, int angles) {
     Aligned al;
     const int vw = pb / (int)esz;
     for (const qknorm_operand_t* o : ops) {
       if (!o) continue;
       al.need(o->x, pb);
       al.need(o->ld_x * esz, pb);
-      if (o->y && !(four && o != q)) {
+      if (o->y && !(four && o != q && pb < 16)) {
         al.need(o->y, pb);
         al.need(o->ld_y * esz, pb);
       }
@@ -352,27 +371,32 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
       al.need(cache->head_stride * esz, pb);
       al.need(cache->token_stride * esz, pb);
     }
-    return al.ok && table_aligned(rope, vw);
+    return al.ok && table_aligned(rope, angles);
   });
   RopePlan& p = out->plan;
   RopeArgs& a = out->args;
   std::memset(&a, 0, sizeof a);
-  int n = 0;
+  int slots_in[3] = {0, 0, 0};
   for (int c = 0; c < 3; ++c) {
-    a.first[c] = n;
     const qknorm_operand_t* o = ops[c];
     if (!o) continue;
     a.side[c] = RopeSide{o->x, o->y, c < 2 ? o->gamma : nullptr, o->ld_x, o->ld_y, (int)(o->h / head_dim)};
-    n += slots_of(a.side[c].heads, p);
+    slots_in[c] = slots_of(a.side[c].heads, p);
   }
-  a.n_slots = n;
-  plan_waves(&p, n, T);
+  plan_waves(&p, slots_in, T);
+  p.apart = four && q && p.whole && p.slots > 1;
+  a.n_slots = slots_in[0] + slots_in[1] + slots_in[2];
+  const int unit = p.whole ? p.slots : 1;   // sides begin at whole waves, or at slots
+  a.first[1] = (slots_in[0] + unit - 1) / unit;
+  a.first[2] = a.first[1] + (slots_in[1] + unit - 1) / unit;
   a.T = T;
   a.gstride = gstride;
   a.head_dim = (int)head_dim;
   a.pairs = p.pairs;
   table_args(rope, p, &a.rot, &a.rot_pairs, &a.cos_sin, &a.ld_table, &a.n_positions, &a.positions);
   a.log2_lanes = log2_of(p.lanes);
+  a.half_lanes = rot && !inter ? (int)(rot / 2 / p.vw) : 0;
+  a.idle = p.lanes * p.np * 2 * p.vw != head_dim;
   a.waves = p.waves;
   a.tokens = p.tokens;
   a.waves_inv = (uint32_t)((65536 + p.waves - 1) / p.waves);
@@ -400,10 +424,10 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
 }
 
 // ------------------------------------------------------------------ backward
-// Blocks per slot of heads: enough to fill the chip's 256 compute units twice
-// over all slots, and no more than there are tokens for the blocks' waves.
+// Blocks per slot of heads: enough to fill the chip's 256 compute units three
+// times over all slots, and no more than there are tokens for the blocks' waves.
 int grad_workers(int n_slots, int64_t T) {
-  int64_t w = (512 + n_slots - 1) / n_slots;
+  int64_t w = (768 + n_slots - 1) / n_slots;
   const int64_t most = (T + kGradWaves - 1) / kGradWaves;
   if (w > most) w = most;
   return (int)(w < 1 ? 1 : w);
@@ -415,8 +439,8 @@ int grad_workers(int n_slots, int64_t T) {
 size_t grad_workspace(int64_t heads_q, int64_t heads_k, int64_t T, int dtype, int64_t head_dim, int64_t gstride) {
   size_t most = 0;
   const int esz = row_elem_bytes(dtype);
-  for (int pb : {16, 8, esz}) {
-    const int vw = pb / esz;
+  for (int pb : {32, 16, 8, esz}) {   // 32: one 16-byte chunk per lane, half a pair
+    const int vw = pb == 32 ? 8 / esz : pb / esz;
     RopePlan p;
     p.pairs = (int)((head_dim + 2 * vw - 1) / (2 * vw));
     p.lanes = 1;
@@ -490,7 +514,7 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
   }
 
   const int64_t rot = rope ? rope->rot_dim : 0;
-  *plan = plan_pieces(dtype, head_dim, rot, rot && rope->interleaved, [&](int pb) {
+  *plan = plan_pieces(dtype, head_dim, rot, rot && rope->interleaved, [&](int pb, int angles) {
     Aligned al;
     const int vw = pb / (int)esz;
     for (const qknorm_grad_operand_t* o : ops) {
@@ -504,7 +528,7 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
       al.need(o->gamma, g);
       al.need(gstride * gsz, g);
     }
-    return al.ok && table_aligned(rope, vw);
+    return al.ok && table_aligned(rope, angles);
   });
   RopeGradArgs& a = *args;
   std::memset(&a, 0, sizeof a);
@@ -523,6 +547,8 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
   a.pairs = plan->pairs;
   table_args(rope, *plan, &a.rot, &a.rot_pairs, &a.cos_sin, &a.ld_table, &a.n_positions, &a.positions);
   a.log2_lanes = log2_of(plan->lanes);
+  a.half_lanes = rot && !rope->interleaved ? (int)(rot / 2 / plan->vw) : 0;
+  a.idle = plan->lanes * plan->np * 2 * plan->vw != head_dim;
   a.workers = grad_workers(a.n_slots, T);
   a.inv_div = (float)(1.0 / (double)head_dim);
   a.eps = eps;

@@ -11,499 +11,452 @@
 // Each element is read once and written once; what a lane needs of the table
 // is loaded once per token and used for every head the wave holds.
 //
-// Work layout (RopePlan in qknorm_ops.hpp): a lane owns pairs of pieces (A, B)
-// of one head. For the half-split rotation A lies in the first half and B in
-// the second, at the same offset, so both members of every pair are in one
-// lane and the rotation needs no exchange between lanes; a wave's A loads
-// cover the first halves of 64 / lanes heads (128 bytes each for 128 bf16
-// columns) and its B loads the second halves. The head's sum of squares is a
-// butterfly over its lanes. One pass of a wave over 64 / lanes heads is a
-// slot; slots never mix Q, K and V, so all that depends on the side is
-// scalar.
+// Work layout: a head of L 16-byte chunks, L a power of two (128 bf16 columns:
+// 16), is held by L neighbouring lanes, one chunk each, so that every load and
+// store of a wave covers 1 KiB in a row (64 / L heads: a slot). For the
+// half-split rotation the other member of a lane's pairs is L/2 lanes away
+// (rot/2 columns), a DPP move inside a 16-lane row and a permlane swap across
+// rows. The first layout tried kept both members of a pair in one lane, which
+// needs no exchange but reads a head in two 128-byte runs per instruction.
+// 8192 tokens x 48 heads x 128 bf16 columns: half-split 39.0 -> 37.0 us (5.6
+// TB/s), interleaved 45 -> 36.6, no rotation 43 -> 36; gradients 79 -> 59.
+// Slots never mix Q, K and V, so all that depends on the side is scalar. Other
+// heads take the layout of qknorm_rope_paired.hip.
 
-#include <hip/hip_runtime.h>
-#include <stdint.h>
+#include "qknorm_rope_device.hpp"
 
 #include <string>
-
-#include "qknorm_device.hpp"
-#include "qknorm_internal.hpp"
-#include "qknorm_ops.hpp"
 
 namespace qkn {
 namespace {
 
-typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-// BYTES bytes at p (aligned to min(BYTES, 16)) into words; smaller elements
-// land in the low bits of the first word.
-template <int BYTES, bool STREAM>
-__device__ __forceinline__ void load_bytes(const char* p, uint32_t* w) {
-  if constexpr (BYTES >= 16) {
+// The value of the lane H away (H a power of two: lane ^ H).
+template <int H>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+  const int i = (int)v;
+  if constexpr (H == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, false);   // quad_perm 1,0,3,2
+  if constexpr (H == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, false);   // quad_perm 2,3,0,1
+  if constexpr (H == 4) {   // row_shl:4 into banks 0 and 2, row_shr:4 into banks 1 and 3
+    const int up = __builtin_amdgcn_update_dpp(0, i, 0x104, 0xF, 0x5, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(up, i, 0x114, 0xF, 0xA, false);
+  }
+  if constexpr (H == 8) return (uint32_t)__builtin_amdgcn_update_dpp(0, i, 0x128, 0xF, 0xF, false);  // row_ror:8
+  if constexpr (H == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return threadIdx.x & 16 ? p[0] : p[1];
+  }
+  const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return threadIdx.x & 32 ? p[0] : p[1];
+}
+template <int H, int VW>
+__device__ __forceinline__ void fetch(const float (&z)[VW], float (&p)[VW]) {
 #pragma unroll
-    for (int q = 0; q < BYTES / 16; ++q) {
-      const u32x4_t* src = reinterpret_cast<const u32x4_t*>(p) + q;
-      const u32x4_t v = STREAM ? __builtin_nontemporal_load(src) : *src;
-      w[4 * q] = v.x;
-      w[4 * q + 1] = v.y;
-      w[4 * q + 2] = v.z;
-      w[4 * q + 3] = v.w;
-    }
-  } else if constexpr (BYTES == 8) {
-    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-  } else if constexpr (BYTES == 4) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (BYTES == 2) {
-    w[0] = *reinterpret_cast<const uint16_t*>(p);
-  } else {
-    w[0] = *reinterpret_cast<const uint8_t*>(p);
+  for (int e = 0; e < VW; ++e) p[e] = __uint_as_float(from_lane<H>(__float_as_uint(z[e])));
+}
+template <int H, int VW>
+__device__ __forceinline__ void fetch(const double (&z)[VW], double (&p)[VW]) {
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, z[e]);
+    p[e] = __builtin_bit_cast(double, (uint64_t)from_lane<H>((uint32_t)(u >> 32)) << 32 | from_lane<H>((uint32_t)u));
   }
 }
 
-template <int BYTES>
-__device__ __forceinline__ void store_bytes(char* p, const uint32_t* w) {
-  if constexpr (BYTES == 16) {
-    const u32x4_t v = {w[0], w[1], w[2], w[3]};
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
-  } else if constexpr (BYTES == 8) {
-    const u32x2_t v = {w[0], w[1]};
-    *reinterpret_cast<u32x2_t*>(p) = v;
-  } else if constexpr (BYTES == 4) {
-    *reinterpret_cast<uint32_t*>(p) = w[0];
-  } else if constexpr (BYTES == 2) {
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
-  } else {
-    *reinterpret_cast<uint8_t*>(p) = (uint8_t)w[0];
-  }
-}
-
-template <int BYTES>
-struct Piece {
-  uint32_t w[BYTES >= 4 ? BYTES / 4 : 1];
-};
-
-// A piece of row data as float32 (exact).
-template <class IO, int VW>
-__device__ __forceinline__ void widen(const uint32_t* w, float (&v)[VW]) {
-  if constexpr (IO::kBytes == 4) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = __uint_as_float(w[e]);
-  } else if constexpr (IO::kBytes == 2) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-  } else if constexpr (VW == 1) {
-    v[0] = __builtin_amdgcn_cvt_pk_f32_fp8(w[0], false)[0];
-  } else {
-#pragma unroll
-    for (int p = 0; p < VW / 4; ++p) {
-      const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[p], false);
-      const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[p], true);
-      v[4 * p] = lo[0];
-      v[4 * p + 1] = lo[1];
-      v[4 * p + 2] = hi[0];
-      v[4 * p + 3] = hi[1];
-    }
-  }
-}
-
-// gamma of a piece as float32: bf16, or float32 for float32 rows.
-template <class IO, int VW>
-__device__ __forceinline__ void widen_gamma(const uint32_t* w, float (&v)[VW]) {
-#pragma unroll
-  for (int e = 0; e < VW; ++e)
-    v[e] = IO::kGBytes == 4 ? __uint_as_float(w[e]) : (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-}
-
-// float32 -> a piece of the row type, one rounding to nearest even (FP8
-// saturates to +-448, NaN stays NaN).
-template <class IO, int VW>
-__device__ __forceinline__ void narrow(const float (&v)[VW], uint32_t* w) {
-  if constexpr (IO::kBytes == 4) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) w[e] = __float_as_uint(v[e]);
-  } else if constexpr (IO::kBytes == 2) {
-    if constexpr (VW == 1) {
-      const f32x2_t f = {v[0], 0.0f};
-      w[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
-    } else {
-#pragma unroll
-      for (int p = 0; p < VW / 2; ++p) {
-        const f32x2_t f = {v[2 * p], v[2 * p + 1]};
-        w[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
-      }
-    }
-  } else if constexpr (VW == 1) {
-    w[0] = pack_fp8_word(sat_e4m3(v[0]), 0.0f, 0.0f, 0.0f);
-  } else {
-#pragma unroll
-    for (int p = 0; p < VW / 4; ++p)
-      w[p] = pack_fp8_word(sat_e4m3(v[4 * p]), sat_e4m3(v[4 * p + 1]), sat_e4m3(v[4 * p + 2]), sat_e4m3(v[4 * p + 3]));
-  }
-}
-
-// Where a lane's pairs lie in a head. Rotated pairs come first: half-split,
-// piece p of each half; interleaved (and the columns past `rot`), two
-// neighbouring pieces. The cos and sin of pair p start at p * VW for both.
-template <int VW, int NP, bool INTER>
-struct Place {
-  int a[NP], b[NP];
-  int tab[NP];        // offset of the pair's cos (0 where not rotated)
-  bool turn[NP];      // rotated
-  bool has_a[NP], has_b[NP];
-  __device__ __forceinline__ Place(int lane_in_head, int lanes, int pairs, int rot_pairs, int rot, int head_dim) {
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int p = lane_in_head + k * lanes;
-      turn[k] = p < rot_pairs;
-      a[k] = INTER || !turn[k] ? 2 * p * VW : p * VW;
-      b[k] = INTER || !turn[k] ? a[k] + VW : (rot >> 1) + p * VW;
-      tab[k] = turn[k] ? p * VW : 0;
-      has_a[k] = p < pairs;
-      has_b[k] = has_a[k] && (VW > 1 || b[k] < head_dim);
-      a[k] = has_a[k] ? a[k] : 0;   // idle: reads the head's first piece
-      b[k] = has_b[k] ? b[k] : 0;
-    }
+// A lane's chunk of a head and its part in the rotation.
+template <int VW, bool INTER>
+struct Chunk1 {
+  static constexpr int TW = INTER ? VW / 2 : VW;   // angles of a chunk
+  int col;           // first column in the head
+  int tab;           // offset of its angles in a table row
+  bool turned;       // rotated
+  uint32_t flip;     // sign bit for the sine: the first member of a pair subtracts
+  __device__ __forceinline__ Chunk1(int lane_in_head, int rot, int half_lanes) {
+    col = lane_in_head * VW;
+    turned = col < rot;
+    tab = !turned ? 0 : INTER ? col / 2 : (lane_in_head & (half_lanes - 1)) * VW;
+    flip = !INTER && lane_in_head < half_lanes ? 0x80000000u : 0u;
   }
 };
 
-// cos and sin of the lane's pairs at one position. A position outside the
-// table gives NaN, which reaches every rotated column of the token.
-template <int VW, int NP, bool INTER>
-struct Angles {
-  float c[NP][VW], s[NP][VW];
-  __device__ __forceinline__ void load(const float* table, int64_t ld, int64_t n, int64_t pos, int half,
-                                       const Place<VW, NP, INTER>& at) {
-    const bool in = pos >= 0 && pos < n;
+// cos and sin for a lane's chunk at one position (half-split: the sine with
+// the sign its member takes). A position outside the table gives NaN, which
+// reaches every rotated column of the token.
+template <int VW, bool INTER>
+struct Turn {
+  static constexpr int TW = Chunk1<VW, INTER>::TW;
+  float c[TW], s[TW];
+  bool in;
+  __device__ __forceinline__ void load(const float* table, int64_t ld, int64_t n, int64_t pos, int half, int tab) {
+    in = pos >= 0 && pos < n;
     const float* row = table + (in ? pos : 0) * ld;
+    load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + tab), reinterpret_cast<uint32_t*>(c));
+    load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + half + tab), reinterpret_cast<uint32_t*>(s));
+  }
+  __device__ __forceinline__ void settle(const Chunk1<VW, INTER>& at) {
+    if (!in) {
+      keep_branch();
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      load_bytes<VW * 4, false>(reinterpret_cast<const char*>(row + at.tab[k]), reinterpret_cast<uint32_t*>(c[k]));
-      load_bytes<VW * 4, false>(reinterpret_cast<const char*>(row + half + at.tab[k]),
-                                reinterpret_cast<uint32_t*>(s[k]));
-      if (!in) {
+      for (int e = 0; e < TW; ++e) c[e] = s[e] = __builtin_nanf("");
+    }
+    if constexpr (!INTER) {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) c[k][e] = s[k][e] = __builtin_nanf("");
-      }
+      for (int e = 0; e < TW; ++e) s[e] = __uint_as_float(__float_as_uint(s[e]) ^ at.flip);
     }
   }
 };
 
-// Rotates one lane's pieces of a head (BACK: by the opposite angle, the
-// transposed map that gradients take).
-template <class F, int VW, bool INTER, bool BACK>
-__device__ __forceinline__ void rotate(F (&a)[VW], F (&b)[VW], const float (&c)[VW], const float (&s)[VW]) {
-  if constexpr (INTER && VW > 1) {
+// Rotates a lane's chunk (BACK: by the opposite angle, the transposed map that
+// gradients take). half_lanes: lanes between the members of a pair. With MAG,
+// `mag` gets the magnitudes that each result is the sum of.
+template <bool BACK, bool MAG, class F, int VW, bool INTER>
+__device__ __forceinline__ void rotate_chunk(F (&z)[VW], const Turn<VW, INTER>& t, const Chunk1<VW, INTER>& at,
+                                             int half_lanes, bool partial, float (&mag)[VW]) {
+  F y[VW], p[VW];
+  if constexpr (INTER) {
 #pragma unroll
     for (int i = 0; i < VW / 2; ++i) {
-      const F ca = c[i], sa = BACK ? -s[i] : s[i], cb = c[VW / 2 + i], sb = BACK ? -s[VW / 2 + i] : s[VW / 2 + i];
-      const F a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-      a[2 * i] = a0 * ca - a1 * sa;
-      a[2 * i + 1] = a1 * ca + a0 * sa;
-      b[2 * i] = b0 * cb - b1 * sb;
-      b[2 * i + 1] = b1 * cb + b0 * sb;
+      const F c = t.c[i], s = BACK ? -t.s[i] : t.s[i];
+      y[2 * i] = z[2 * i] * c - z[2 * i + 1] * s;
+      y[2 * i + 1] = z[2 * i + 1] * c + z[2 * i] * s;
+      p[2 * i] = z[2 * i + 1];
+      p[2 * i + 1] = z[2 * i];
     }
   } else {
+    switch (half_lanes) {   // uniform over the launch
+      case 8: fetch<8>(z, p); break;
+      case 4: fetch<4>(z, p); break;
+      case 16: fetch<16>(z, p); break;
+      case 2: fetch<2>(z, p); break;
+      case 1: fetch<1>(z, p); break;
+      default: fetch<32>(z, p); break;
+    }
+#pragma unroll
+    for (int e = 0; e < VW; ++e) y[e] = z[e] * (F)t.c[e] + p[e] * (F)(BACK ? -t.s[e] : t.s[e]);
+  }
+  if constexpr (MAG) {
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      const F ce = c[e], se = BACK ? -s[e] : s[e];
-      const F a0 = a[e], b0 = b[e];
-      a[e] = a0 * ce - b0 * se;
-      b[e] = b0 * ce + a0 * se;
+      const int i = INTER ? e / 2 : e;
+      const float m = __builtin_fmaf(__builtin_fabsf((float)z[e]), __builtin_fabsf(t.c[i]),
+                                     __builtin_fabsf((float)p[e]) * __builtin_fabsf(t.s[i]));
+      mag[e] = partial && !at.turned ? mag[e] : m;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) z[e] = partial && !at.turned ? z[e] : y[e];
+}
+
+// MXFP4: per 32 channels the scale 2^E with E = floor(log2(largest)) - 2 held
+// to [-100, 125], and E2M1 codes rounded to nearest even, magnitudes past 6
+// saturating. 32 / VW lanes hold a block. One that holds an infinity or NaN
+// gets the scale byte 0xFF and reads as NaN.
+template <int VW>
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
+  if (VW == 4) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
+  return m;
+}
+// The scale byte of a block whose largest magnitude has these bits (NaN above infinity).
+__device__ __forceinline__ int scale_byte(uint32_t m) {
+  return m >= 0x7F800000u ? 0xFF : min(max((int)(m >> 23) - 2, 27), 252);
+}
+__device__ __forceinline__ float over_scale(int byte) {   // 2^-E
+  return __uint_as_float((uint32_t)(254 - (byte == 0xFF ? 127 : byte)) << 23);
+}
+template <int VW>
+__device__ __forceinline__ uint32_t codes_of(const float (&a)[VW]) {   // already over the scale
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[0], a[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[2], a[3], 1.0f, 1);
+  if constexpr (VW == 8) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[4], a[5], 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[6], a[7], 1.0f, 3);
+  }
+  return w;
+}
+struct Coded {
+  uint32_t w;
+  int byte;
+};
+
+// The codes of a lane's values.
+template <int VW>
+__device__ __forceinline__ Coded quantize(const float (&f)[VW]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+  Coded q;
+  q.byte = scale_byte(block_max<VW>(m));
+  const float inv = over_scale(q.byte);
+  float a[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) a[e] = q.byte == 0xFF ? 0.0f : f[e] * inv;
+  q.w = codes_of<VW>(a);
+  return q;
+}
+
+// The codes of values known to within kUnsure of `mag`: true if every value
+// within that distance has them (in this lane's share of its block).
+constexpr float kUnsure = 0x1p-19f;
+template <int VW>
+__device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float (&mag)[VW], Coded& q) {
+  float lo[VW], hi[VW];
+  uint32_t ml = 0, mh = 0;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    const float v = __builtin_fabsf(f[e]);
+    hi[e] = __builtin_fmaf(mag[e], kUnsure, v);
+    lo[e] = __builtin_fmaf(mag[e], -kUnsure, v);
+    lo[e] = lo[e] > 0.0f ? lo[e] : 0.0f;        // NaN: 0, which differs from hi's
+    ml = max(ml, __float_as_uint(lo[e]));
+    mh = max(mh, __float_as_uint(hi[e]) & 0x7FFFFFFFu);
+  }
+  ml = block_max<VW>(ml);
+  mh = block_max<VW>(mh);
+  q.byte = scale_byte(mh);
+  if (mh >= 0x7F800000u || scale_byte(ml) != q.byte) return false;
+  const float inv = over_scale(q.byte);
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    hi[e] = __builtin_copysignf(hi[e] * inv, f[e]);
+    lo[e] = __builtin_copysignf(lo[e] * inv, f[e]);
+  }
+  q.w = codes_of<VW>(hi);
+  return q.w == codes_of<VW>(lo);
+}
+
+// A lane's normalized and rotated chunk formed in float64 and rounded to odd,
+// four elements at a time to keep registers for waves.
+template <class IO, bool INTER>
+__device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, const char* gamma, int64_t pos, bool turns,
+                                            const Chunk1<IO::kVW, INTER>& at, int L, float (&f)[IO::kVW]) {
+  constexpr int VW = IO::kVW;
+  constexpr int GB = VW * IO::kGBytes;
+  float v[VW], g[VW];
+  {
+    Piece<16> w;
+    load_bytes<16, false>(x, w.w);
+    widen<IO, VW>(w.w, v);
+    if (gamma) {
+      Piece<GB> wg;
+      load_bytes<GB, false>(gamma, wg.w);
+      widen_gamma<IO, VW>(wg.w, g);
+    }
+  }
+  double r = 1.0;
+  if (gamma) {
+    double ss = 0.0;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) ss = __builtin_fma((double)v[e], (double)v[e], ss);
+    ss = group_sum_d(ss, L);
+    r = 1.0 / __builtin_sqrt(ss / a.head_dim + (double)a.eps);
+  }
+  const bool in = pos >= 0 && pos < a.n_positions;
+  const float* row = turns ? a.cos_sin + (in ? pos : 0) * a.ld_table + at.tab : nullptr;
+#pragma unroll 1
+  for (int e0 = 0; e0 < VW; e0 += 4) {
+    double z[4], p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float one = VW > 4 && e0 ? v[(k + 4) % VW] : v[k];
+      z[k] = one;
+      if (gamma) z[k] = z[k] * (VW > 4 && e0 ? g[(k + 4) % VW] : g[k]) * r;
+    }
+    if (turns) {
+      if constexpr (INTER) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = z[k ^ 1];
+      } else {
+        switch (a.half_lanes) {
+          case 8: fetch<8>(z, p); break;
+          case 4: fetch<4>(z, p); break;
+          case 16: fetch<16>(z, p); break;
+          case 2: fetch<2>(z, p); break;
+          case 1: fetch<1>(z, p); break;
+          default: fetch<32>(z, p); break;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = INTER ? (e0 + k) >> 1 : e0 + k;
+        const double c = in ? row[i] : __builtin_nanf(""), sn = in ? row[(a.rot >> 1) + i] : __builtin_nanf("");
+        const bool first = INTER ? (k & 1) == 0 : at.flip != 0;   // of its pair: the sine is subtracted
+        const double y = z[k] * c + p[k] * (first ? -sn : sn);
+        p[k] = at.turned ? y : z[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = z[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float one = round_to_odd(p[k]);
+      if (VW > 4 && e0)
+        f[(k + 4) % VW] = one;
+      else
+        f[k] = one;
     }
   }
 }
 
-// float64 sums over a head's lanes, by the same steps as group_sum.
-template <int CTRL>
-__device__ __forceinline__ double dpp_move_d(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-__device__ __forceinline__ double swap_add_d(double v, bool across32) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
-  const auto l = across32 ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
-                          : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-  const auto h = across32 ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
-                          : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-  return __builtin_bit_cast(double, ((uint64_t)h[0] << 32) | l[0]) +
-         __builtin_bit_cast(double, ((uint64_t)h[1] << 32) | l[1]);
-}
-__device__ __forceinline__ double group_sum_d(double v, int group) {
-  if (group > 1) v += dpp_move_d<0xB1>(v);
-  if (group > 2) v += dpp_move_d<0x4E>(v);
-  if (group > 4) v += dpp_move_d<0x141>(v);
-  if (group > 8) v += dpp_move_d<0x140>(v);
-  if (group > 16) v = swap_add_d(v, false);
-  if (group > 32) v = swap_add_d(v, true);
-  return v;
-}
-
-// float64 -> float32 rounded to odd: truncated, and the last bit set if
-// anything was lost. Rounding that once more to a format of at least two bits
-// fewer gives what rounding the float64 value once would have given.
-__device__ __forceinline__ float round_to_odd(double z) {
-  const float f = (float)z;
-  const double back = (double)f;
-  uint32_t u = __float_as_uint(f);
-  if (__builtin_fabs(back) > __builtin_fabs(z)) u -= 1;      // toward zero (infinity: to the largest)
-  if (back != z && z == z) u |= 1;
-  return __uint_as_float(u);
-}
-
-// Most float32 values of one slot's heads (one wave's exchange buffer).
-constexpr int kSlotValues = 1024;
-constexpr int kRopeMaxWaves = 8;
-
-// One wave's slot of K or V values, float32 in `val` ([heads][head_dim]),
-// into MXFP4: per 32 channels the scale 2^E with E = floor(log2(largest)) - 2
-// held to [-100, 125], and E2M1 codes rounded to nearest even, magnitudes
-// past 6 saturating. Four lanes hold a block, eight channels each. A block
-// that holds an infinity or NaN gets the scale byte 0xFF and reads as NaN.
-template <class IO>
-__device__ __forceinline__ void quantize_slot(const float* val, const RopeArgs& a, int lane, int heads_here,
-                                              int head0, char* codes, char* scales, char* y_row) {
-  const int per_head = a.head_dim >> 3;   // eight-channel pieces
-  const int total = heads_here * per_head;
-#pragma unroll 1
-  for (int i0 = 0; i0 < total; i0 += 64) {
-    const int i = i0 + lane;
-    const bool on = i < total;            // the same for the four lanes of a block
-    const int h = on ? i / per_head : 0;
-    const int c = on ? (i - h * per_head) * 8 : 0;
-    float f[8];
-#pragma unroll
-    for (int q = 0; q < 8; q += 4) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(val + h * a.head_dim + c + q);
-      f[q] = v[0];
-      f[q + 1] = v[1];
-      f[q + 2] = v[2];
-      f[q + 3] = v[3];
-    }
-    uint32_t m = 0;                       // largest magnitude, as ordered bits: NaN above infinity
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
-    const bool bad = m >= 0x7F800000u;
-    const int byte = bad ? 0xFF : min(max((int)(m >> 23) - 2, 27), 252);
-    const float inv = __uint_as_float((uint32_t)(254 - (bad ? 127 : byte)) << 23);
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = bad ? 0.0f : f[e] * inv;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], 1.0f, 3);
-    if (on) {
-      *reinterpret_cast<uint32_t*>(codes + (int64_t)(head0 + h) * a.head_stride + (c >> 1)) = w;
-      if ((lane & 3) == 0) scales[(int64_t)(head0 + h) * a.scale_head_stride + (c >> 5)] = (char)byte;
-      if (y_row) {   // what the cache now holds, in the row type (exact)
-        const float scale = __uint_as_float(bad ? 0x7FC00000u : (uint32_t)byte << 23);
-        float y[8];
-        const f32x2_t y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-        const f32x2_t y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-        const f32x2_t y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-        const f32x2_t y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-        y[0] = y0[0] * scale, y[1] = y0[1] * scale, y[2] = y1[0] * scale, y[3] = y1[1] * scale;
-        y[4] = y2[0] * scale, y[5] = y2[1] * scale, y[6] = y3[0] * scale, y[7] = y3[1] * scale;
-        uint32_t o[IO::kBytes * 2];
-        narrow<IO, 8>(y, o);
-        char* p = y_row + ((int64_t)(head0 + h) * a.head_dim + c) * IO::kBytes;
-        if (a.y_wide) {
-#pragma unroll
-          for (int q = 0; q < IO::kBytes / 2; ++q) store_bytes<16>(p + 16 * q, o + 4 * q);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t one = IO::kBytes == 4 ? o[e] : o[e >> 1] >> (16 * (e & 1));
-            store_bytes<IO::kBytes>(p + e * IO::kBytes, &one);
-          }
-        }
-      }
-    }
+// The values that codes stand for.
+template <int VW>
+__device__ __forceinline__ void coded_values(const Coded& q, float (&f)[VW]) {
+  const float back = __uint_as_float(q.byte == 0xFF ? 0x7FC00000u : (uint32_t)q.byte << 23);
+  const f32x2_t y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 0);
+  const f32x2_t y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 1);
+  f[0] = y0[0] * back, f[1] = y0[1] * back, f[2] = y1[0] * back, f[3] = y1[1] * back;
+  if constexpr (VW == 8) {
+    const f32x2_t y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 2);
+    const f32x2_t y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 3);
+    f[4] = y2[0] * back, f[5] = y2[1] * back, f[6] = y3[0] * back, f[7] = y3[1] * back;
   }
 }
 
 // The forward pass (MODE ROPE_FORWARD: Q and K rows to y) and the append
-// calls (Q to y, K and V into the cache). Block: `waves` waves per token,
-// each with S slots of it, `tokens` tokens; grid.y covers the slots past a
-// block's waves. All loads of a wave's slots are issued before the first is
-// used.
-template <class IO, int PB, int NP, int S, bool INTER, int MODE>
-__global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_rows(const RopeArgs a) {
-  constexpr int VW = PB / IO::kBytes;
+// calls (Q to y, K and V into the cache). A wave takes one token's next S
+// slots of one side; which, its number says (a.groups waves per token). All of
+// a wave's rows are loaded before the first is used, and the angles serve all
+// its slots.
+template <class IO, int S, bool INTER, int MODE>
+__global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeArgs a) {
+  constexpr int VW = IO::kVW;
   constexpr int GB = VW * IO::kGBytes;
-  __shared__ __align__(16) float exchange[MODE == ROPE_APPEND_MXFP4 ? kRopeMaxWaves * kSlotValues : 4];
+  constexpr uint32_t XR = 16;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tok = (int)((uint32_t)wave * a.waves_inv >> 16);           // wave / waves
-  const int slot0 = (blockIdx.y * a.waves + (wave - tok * a.waves)) * S;
-  if (slot0 >= a.n_slots) return;
+  // each run of 8 * XR blocks transposed: the hardware deals blocks to the 8
+  // XCDs in turn, and XR consecutive ones (tokens side by side in the cache's
+  // pages) then meet in one L2
+  uint32_t block = blockIdx.x;
+  if (block < (gridDim.x & ~(8u * XR - 1)))
+    block = (block & ~(8u * XR - 1)) | ((block & 7) * XR) | ((block >> 3) & (XR - 1));
+  const uint32_t unit = block * kRopeWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= a.units) return;
+  const uint32_t t0 = over(unit, a.by_groups);
+  const int group = unit - t0 * a.by_groups.d;
+  const int c = group < a.first[1] ? 0 : MODE != ROPE_FORWARD && group >= a.first[2] ? 2 : 1;   // Q, K or V
+  const RopeSide& o = a.side[c];
   const int L = 1 << a.log2_lanes;
-  const int hl = lane >> a.log2_lanes;
   const int hw = 64 >> a.log2_lanes;
-  const Place<VW, NP, INTER> at(lane & (L - 1), L, a.pairs, a.rot_pairs, a.rot, a.head_dim);
+  const int head0 = (group - a.first[c]) * S * hw + (lane >> a.log2_lanes);   // of the first slot
+  const Chunk1<VW, INTER> at(lane & (L - 1), a.rot, a.half_lanes);
+  const bool partial = a.rot < a.head_dim;
+  const bool turns = a.rot != 0 && c != 2;
 
-  const int64_t step = (int64_t)gridDim.x * a.tokens;
-  for (int64_t t = (int64_t)blockIdx.x * a.tokens + tok; t < a.T; t += step) {
-    int64_t place = 0;
-    if constexpr (MODE != ROPE_FORWARD) {
-      place = load_uniform(a.slots + t);
-      if (place < 0 || place >= a.n_tokens_held) continue;   // a row that holds no token
+  const char* gamma = static_cast<const char*>(c == 2 ? nullptr : o.gamma);
+  Piece<GB> gam;   // of the first slot: of all where heads share it
+  if (gamma) load_bytes<GB, false>(gamma + ((head0 < o.heads ? head0 : 0) * a.gstride + at.col) * IO::kGBytes, gam.w);
+  uint32_t off[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int head = head0 + i * hw;
+    off[i] = (uint32_t)((head < o.heads ? head : 0) * a.head_dim + at.col) * IO::kBytes;   // idle lanes: the first head
+  }
+
+  // Slot i's results (codes in q, for a cache of them) to where they go.
+  const auto store = [&](int i, bool on, float (&f)[VW], const Coded& q, int64_t t, int64_t place) {
+    const int64_t head = head0 + i * hw;
+    if (MODE != ROPE_FORWARD && c != 0) {
+      const int64_t page = place >> a.log2_page, in = place & (((int64_t)1 << a.log2_page) - 1);
+      char* p = a.cache[c - 1] + page * a.page_stride + in * a.token_stride + head * a.head_stride;
+      if constexpr (MODE == ROPE_APPEND_MXFP4) {
+        char* sc = a.scales[c - 1] + page * a.scale_page_stride + in * (a.head_dim >> 5) + head * a.scale_head_stride;
+        if (on) {
+          store_bytes<VW / 2>(p + (at.col >> 1), &q.w);
+          if ((lane & (32 / VW - 1)) == 0) sc[at.col >> 5] = (char)q.byte;
+        }
+        if (o.y) coded_values<VW>(q, f);
+      } else {
+        Piece<16> w;
+        narrow<IO, VW>(f, w.w);
+        if (on) store_bytes<16>(p + at.col * IO::kBytes, w.w);
+      }
     }
-    Piece<PB> xa[S][NP], xb[S][NP];
-    Piece<GB> ga[S][NP], gb[S][NP];
+    if (o.y) {
+      Piece<16> w;
+      narrow<IO, VW>(f, w.w);
+      if (on) store_bytes<16>(static_cast<char*>(o.y) + t * o.ldy * IO::kBytes + (head * a.head_dim + at.col) * IO::kBytes, w.w);
+    }
+  };
+
+  for (int64_t t = t0; t < a.T; t += a.tokens) {
+    uint32_t unsure = 0;   // slots whose codes float32 leaves open
+    // A row that holds no token is worked like the others, and not stored: its
+    // slot, waited for first, would hold up all that follows.
+    int64_t place = 0, pos = 0;
+    if constexpr (MODE != ROPE_FORWARD) place = load_uniform(a.slots + t);
+    if (turns) pos = load_uniform(a.positions + t);
+    Piece<16> x[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      load_bytes<16, true>(static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + off[i], x[i].w);
+    Turn<VW, INTER> turn;
+    if (turns) {
+      turn.load(a.cos_sin, a.ld_table, a.n_positions, pos, a.rot >> 1, at.tab);
+      turn.settle(at);
+    }
+    const bool live = MODE == ROPE_FORWARD || (place >= 0 && place < a.n_tokens_held);
+
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int s = min(slot0 + i, a.n_slots - 1);
-      const int c = s < a.first[1] ? 0 : MODE != ROPE_FORWARD && s >= a.first[2] ? 2 : 1;
-      const RopeSide& o = a.side[c];
-      const int head = (s - a.first[c]) * hw + hl;
-      const int hc = head < o.heads ? head : 0;
-      const char* row = static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes;
-      const char* g = static_cast<const char*>(o.gamma);
+      const bool on = head0 + i * hw < o.heads;
+      if (i > 0 && __builtin_amdgcn_ballot_w64(on) == 0) break;   // the side's last slot is done
+      if (i > 0 && gamma && a.gstride)
+        load_bytes<GB, false>(gamma + ((on ? head0 + i * hw : 0) * a.gstride + at.col) * IO::kGBytes, gam.w);
+      float f[VW];
+      widen<IO, VW>(x[i].w, f);
+      float mag[VW];
+      if (gamma) {
+        float ss = 0.0f;
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        load_bytes<PB, true>(row + (uint32_t)(hc * a.head_dim + at.a[k]) * IO::kBytes, xa[i][k].w);
-        load_bytes<PB, true>(row + (uint32_t)(hc * a.head_dim + at.b[k]) * IO::kBytes, xb[i][k].w);
-      }
-      if (g) {
-        g += hc * a.gstride * IO::kGBytes;
+        for (int e = 0; e < VW; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
+        ss = group_sum(ss, L);
+        const float r = rms_factor(ss, a.inv_div, a.eps);
+        float g[VW];
+        widen_gamma<IO, VW>(gam.w, g);
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          load_bytes<GB, false>(g + at.a[k] * IO::kGBytes, ga[i][k].w);
-          load_bytes<GB, false>(g + at.b[k] * IO::kGBytes, gb[i][k].w);
-        }
+        for (int e = 0; e < VW; ++e) f[e] = (f[e] * g[e]) * r;
       }
-    }
-    Angles<VW, NP, INTER> turn;
-    if (a.rot_pairs) turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
+      if (MODE == ROPE_APPEND_MXFP4) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) mag[e] = __builtin_fabsf(f[e]);
+      }
+      if (turns) rotate_chunk<false, MODE == ROPE_APPEND_MXFP4>(f, turn, at, a.half_lanes, partial, mag);
 
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int s = slot0 + i;
-      if (s >= a.n_slots) break;
-      const int c = s < a.first[1] ? 0 : MODE != ROPE_FORWARD && s >= a.first[2] ? 2 : 1;
-      const RopeSide& o = a.side[c];
-      const int head0 = (s - a.first[c]) * hw;
-      const bool on = head0 + hl < o.heads;
-      float fa[NP][VW], fb[NP][VW];
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        widen<IO, VW>(xa[i][k].w, fa[k]);
-        widen<IO, VW>(xb[i][k].w, fb[k]);
-      }
-      const bool exact = MODE == ROPE_APPEND_MXFP4 && c == 1;
-      if (exact) {
-        // Keys bound for 4-bit codes: formed in float64 (vector float64 runs
-        // at the float32 rate here), so that every code is the one exact
-        // arithmetic gives and does not hang on the order of a sum.
-        double r = 1.0;
-        if (o.gamma) {
-          double ss = 0.0;
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              const double va = at.has_a[k] ? fa[k][e] : 0.0f, vb = at.has_b[k] ? fb[k][e] : 0.0f;
-              ss += va * va + vb * vb;
-            }
-          ss = group_sum_d(ss, L);
-          r = 1.0 / __builtin_sqrt(ss / a.head_dim + (double)a.eps);
-        }
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          double da[VW], db[VW];
-          float gfa[VW], gfb[VW];
-          if (o.gamma) {
-            widen_gamma<IO, VW>(ga[i][k].w, gfa);
-            widen_gamma<IO, VW>(gb[i][k].w, gfb);
-          }
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            da[e] = o.gamma ? (double)fa[k][e] * gfa[e] * r : (double)fa[k][e];
-            db[e] = o.gamma ? (double)fb[k][e] * gfb[e] * r : (double)fb[k][e];
-          }
-          if (at.turn[k]) rotate<double, VW, INTER, false>(da, db, turn.c[k], turn.s[k]);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            fa[k][e] = round_to_odd(da[e]);
-            fb[k][e] = round_to_odd(db[e]);
-          }
-        }
-      } else if (c != 2) {
-        if (o.gamma) {
-          float ss = 0.0f;
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              const float va = at.has_a[k] ? fa[k][e] : 0.0f, vb = at.has_b[k] ? fb[k][e] : 0.0f;
-              ss = __builtin_fmaf(va, va, ss);
-              ss = __builtin_fmaf(vb, vb, ss);
-            }
-          ss = group_sum(ss, L);
-          const float r = rms_factor(ss, a.inv_div, a.eps);
-#pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            float gfa[VW], gfb[VW];
-            widen_gamma<IO, VW>(ga[i][k].w, gfa);
-            widen_gamma<IO, VW>(gb[i][k].w, gfb);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              fa[k][e] = (fa[k][e] * gfa[e]) * r;
-              fb[k][e] = (fb[k][e] * gfb[e]) * r;
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < NP; ++k)
-          if (at.turn[k]) rotate<float, VW, INTER, false>(fa[k], fb[k], turn.c[k], turn.s[k]);
-      }
-
-      char* y_row = o.y ? static_cast<char*>(o.y) + t * o.ldy * IO::kBytes : nullptr;
+      Coded q;
       if (MODE == ROPE_APPEND_MXFP4 && c != 0) {
-        float* ex = exchange + wave * kSlotValues;
-#pragma unroll
-        for (int k = 0; k < NP; ++k)
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            if (at.has_a[k]) ex[hl * a.head_dim + at.a[k] + e] = fa[k][e];
-            if (at.has_b[k]) ex[hl * a.head_dim + at.b[k] + e] = fb[k][e];
-          }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const int64_t page = place >> a.log2_page, off = place & (((int64_t)1 << a.log2_page) - 1);
-        char* codes = a.cache[c - 1] + page * a.page_stride + off * a.token_stride;
-        char* scales = a.scales[c - 1] + page * a.scale_page_stride + off * (a.head_dim >> 5);
-        quantize_slot<IO>(ex, a, lane, min(hw, o.heads - head0), head0, codes, scales, y_row);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        continue;
+        if (c == 2) {
+          q = quantize<VW>(f);
+        } else if (__builtin_amdgcn_ballot_w64(!quantize_sure<VW>(f, mag, q)) != 0) {
+          unsure |= 1u << i;
+          continue;
+        }
       }
-      if (!on) continue;
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        Piece<PB> ya, yb;
-        narrow<IO, VW>(fa[k], ya.w);
-        narrow<IO, VW>(fb[k], yb.w);
-        const int64_t col = (int64_t)(head0 + hl) * a.head_dim;
-        if (MODE == ROPE_APPEND_ROWS && c != 0) {
-          const int64_t page = place >> a.log2_page, off = place & (((int64_t)1 << a.log2_page) - 1);
-          char* p = a.cache[c - 1] + page * a.page_stride + off * a.token_stride + (int64_t)(head0 + hl) * a.head_stride;
-          if (at.has_a[k]) store_bytes<PB>(p + at.a[k] * IO::kBytes, ya.w);
-          if (at.has_b[k]) store_bytes<PB>(p + at.b[k] * IO::kBytes, yb.w);
-        }
-        if (y_row) {
-          if (at.has_a[k]) store_bytes<PB>(y_row + (col + at.a[k]) * IO::kBytes, ya.w);
-          if (at.has_b[k]) store_bytes<PB>(y_row + (col + at.b[k]) * IO::kBytes, yb.w);
-        }
+      store(i, on && live, f, q, t, place);
+    }
+
+    if constexpr (MODE == ROPE_APPEND_MXFP4) {
+      // A key's float32 value is within 16 u of the magnitudes it is the sum
+      // of (r within 11 u: a chain of 8 squares, 6 butterfly adds, the factor;
+      // then 4 roundings), u = 2^-24; kUnsure is twice that. Where a border of
+      // the codes or of the scale lies that near to one (in about 2% of the
+      // slots) the slot is formed again in float64, so that every code is the
+      // one exact arithmetic gives and does not hang on the order of a sum.
+      // Here, behind the others, where little else is held in registers (in
+      // float64 throughout, 8192 tokens took 69 us).
+#pragma unroll 1
+      for (int i = 0; live && unsure != 0; ++i, unsure >>= 1) {
+        if (!(unsure & 1)) continue;
+        const int head = head0 + i * hw;
+        const bool on = head < o.heads;
+        float f[VW];
+        exact_chunk<IO, INTER>(
+            a, static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + (int64_t)((on ? head : 0) * a.head_dim + at.col) * IO::kBytes,
+            gamma ? gamma + ((on ? head : 0) * a.gstride + at.col) * IO::kGBytes : nullptr,
+            pos, turns, at, L, f);
+        const Coded q = quantize<VW>(f);
+        store(i, on, f, q, t, place);
       }
     }
   }
@@ -514,16 +467,15 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_rows(const Rop
 // gamma) of g_j xr_j, and dx = r (gg - xr mean(gg xr)). x and dy are read
 // once, dx written once; everything between stays in registers. A wave keeps
 // one slot of heads for all its tokens, so its share of dgamma stays in
-// registers too and leaves as one partial row per block (eight waves, added
-// in LDS in a fixed order); qknorm_rope_grad_sum adds the rows in a fixed
-// order, so the gradients do not change from run to run. The next token's
-// loads are issued before the current one is worked on.
-template <class IO, int PB, int NP, bool INTER>
+// registers too and leaves as one partial row per block (its waves added in
+// LDS in a fixed order); qknorm_rope_grad_sum adds the rows in a fixed order,
+// so the gradients do not change from run to run. The next token's loads are
+// issued before the current one is worked on.
+template <class IO, bool INTER>
 __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGradArgs a) {
-  constexpr int VW = PB / IO::kBytes;
+  constexpr int VW = IO::kVW;
   constexpr int GB = VW * IO::kGBytes;
-  constexpr int E = 2 * NP * VW;
-  __shared__ float red[kGradWaves * 64 * E];
+  __shared__ float red[kGradWaves * 64 * VW];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int s = blockIdx.y;
@@ -535,129 +487,78 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
   const int head = (s - a.first[c]) * hw + hl;
   const bool on = head < o.heads;
   const int hc = on ? head : 0;
-  const Place<VW, NP, INTER> at(lane & (L - 1), L, a.pairs, a.rot_pairs, a.rot, a.head_dim);
+  const Chunk1<VW, INTER> at(lane & (L - 1), a.rot, a.half_lanes);
+  const bool partial = a.rot < a.head_dim;
+  const uint32_t off = (uint32_t)(hc * a.head_dim + at.col) * IO::kBytes;
 
-  float gfa[NP][VW], gfb[NP][VW];
-  float sa[NP][VW], sb[NP][VW];
-  uint32_t oa[NP], ob[NP];
+  float g[VW], sum[VW];
   {
-    const char* g = static_cast<const char*>(o.gamma) + hc * a.gstride * IO::kGBytes;
+    Piece<GB> p;
+    load_bytes<GB, false>(static_cast<const char*>(o.gamma) + (hc * a.gstride + at.col) * IO::kGBytes, p.w);
+    widen_gamma<IO, VW>(p.w, g);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      Piece<GB> p;
-      load_bytes<GB, false>(g + at.a[k] * IO::kGBytes, p.w);
-      widen_gamma<IO, VW>(p.w, gfa[k]);
-      load_bytes<GB, false>(g + at.b[k] * IO::kGBytes, p.w);
-      widen_gamma<IO, VW>(p.w, gfb[k]);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) sa[k][e] = sb[k][e] = 0.0f;
-      oa[k] = (uint32_t)(hc * a.head_dim + at.a[k]) * IO::kBytes;
-      ob[k] = (uint32_t)(hc * a.head_dim + at.b[k]) * IO::kBytes;
-    }
+    for (int e = 0; e < VW; ++e) sum[e] = 0.0f;
   }
-  const char* x = static_cast<const char*>(o.x);
-  const char* dy = static_cast<const char*>(o.dy);
-  char* dx = static_cast<char*>(o.dx);
 
   struct In {
-    Piece<PB> xa[NP], xb[NP], ya[NP], yb[NP];
-    Angles<VW, NP, INTER> turn;
+    Piece<16> x, dy;
+    Turn<VW, INTER> turn;
   };
   const auto load = [&](In& in, int64_t t) {
-    const char* xr = x + t * o.ldx * IO::kBytes;
-    const char* yr = dy + t * o.lddy * IO::kBytes;
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      load_bytes<PB, true>(xr + oa[k], in.xa[k].w);
-      load_bytes<PB, true>(xr + ob[k], in.xb[k].w);
-      load_bytes<PB, true>(yr + oa[k], in.ya[k].w);
-      load_bytes<PB, true>(yr + ob[k], in.yb[k].w);
-    }
-    if (a.rot_pairs) in.turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
+    load_bytes<16, true>(static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + off, in.x.w);
+    load_bytes<16, true>(static_cast<const char*>(o.dy) + t * o.lddy * IO::kBytes + off, in.dy.w);
+    if (a.rot)
+      in.turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at.tab);
   };
-
-  const int64_t step = (int64_t)a.workers * kGradWaves;
-  int64_t t = (int64_t)blockIdx.x * kGradWaves + wave;
-  In next;
-  if (t < a.T) load(next, t);
-  for (; t < a.T; t += step) {
-    In in = next;
-    if (t + step < a.T) load(next, t + step);
-    float xa[NP][VW], xb[NP][VW], ya[NP][VW], yb[NP][VW];
+  const auto work = [&](In& in, int64_t t) {
+    float x[VW], y[VW], gg[VW];
+    widen<IO, VW>(in.x.w, x);
+    widen<IO, VW>(in.dy.w, y);
+    if (a.rot) {
+      in.turn.settle(at);
+      rotate_chunk<true, false>(y, in.turn, at, a.half_lanes, partial, gg);
+    }
     float ss = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      widen<IO, VW>(in.xa[k].w, xa[k]);
-      widen<IO, VW>(in.xb[k].w, xb[k]);
-      widen<IO, VW>(in.ya[k].w, ya[k]);
-      widen<IO, VW>(in.yb[k].w, yb[k]);
-      if (at.turn[k]) rotate<float, VW, INTER, true>(ya[k], yb[k], in.turn.c[k], in.turn.s[k]);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const float va = at.has_a[k] ? xa[k][e] : 0.0f, vb = at.has_b[k] ? xb[k][e] : 0.0f;
-        ss = __builtin_fmaf(va, va, ss);
-        ss = __builtin_fmaf(vb, vb, ss);
-        const float pa = at.has_a[k] ? ya[k][e] * gfa[k][e] : 0.0f, pb = at.has_b[k] ? yb[k][e] * gfb[k][e] : 0.0f;
-        dot = __builtin_fmaf(pa, va, dot);
-        dot = __builtin_fmaf(pb, vb, dot);
-      }
+    for (int e = 0; e < VW; ++e) {
+      ss = __builtin_fmaf(x[e], x[e], ss);
+      gg[e] = y[e] * g[e];
+      dot = __builtin_fmaf(gg[e], x[e], dot);
     }
     group_sum_qk(ss, dot, L);
     const float r = rms_factor(ss, a.inv_div, a.eps);
     const float mean = (dot * r) * a.inv_div;
-    char* row = dx + t * o.lddx * IO::kBytes;
+    float d[VW];
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      float da[VW], db[VW];
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const float ra = xa[k][e] * r, rb = xb[k][e] * r;
-        sa[k][e] = __builtin_fmaf(ya[k][e], ra, sa[k][e]);
-        sb[k][e] = __builtin_fmaf(yb[k][e], rb, sb[k][e]);
-        da[e] = r * (ya[k][e] * gfa[k][e] - ra * mean);
-        db[e] = r * (yb[k][e] * gfb[k][e] - rb * mean);
-      }
-      if (on) {
-        Piece<PB> p;
-        narrow<IO, VW>(da, p.w);
-        if (at.has_a[k]) store_bytes<PB>(row + oa[k], p.w);
-        narrow<IO, VW>(db, p.w);
-        if (at.has_b[k]) store_bytes<PB>(row + ob[k], p.w);
-      }
+    for (int e = 0; e < VW; ++e) {
+      const float xr = x[e] * r;
+      sum[e] = __builtin_fmaf(y[e], xr, sum[e]);
+      d[e] = r * __builtin_fmaf(-xr, mean, gg[e]);
     }
-  }
+    Piece<16> p;
+    narrow<IO, VW>(d, p.w);
+    if (on) store_bytes<16>(static_cast<char*>(o.dx) + t * o.lddx * IO::kBytes + off, p.w);
+  };
+  each_token<In>((int64_t)blockIdx.x * kGradWaves + wave, (int64_t)a.workers * kGradWaves, a.T, load, work);
 
   if (!o.dgamma) return;
 #pragma unroll
-  for (int k = 0; k < NP; ++k)
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      red[(wave * E + k * 2 * VW + e) * 64 + lane] = sa[k][e];
-      red[(wave * E + (k * 2 + 1) * VW + e) * 64 + lane] = sb[k][e];
-    }
+  for (int e = 0; e < VW; ++e) red[(wave * VW + e) * 64 + lane] = sum[e];
   __syncthreads();
   // Shared gamma: one row per (slot, worker), the slot's heads added too;
   // otherwise one row per (head, worker).
   const bool shared = a.gstride == 0;
   const int live = min(hw, o.heads - (s - a.first[c]) * hw);   // heads of this slot
-  for (int i = threadIdx.x; i < E * 64; i += 64 * kGradWaves) {
+  for (int i = threadIdx.x; i < VW * 64; i += 64 * kGradWaves) {
     const int l = i & 63, e = i >> 6;
     const int lh = l >> a.log2_lanes;
     if (shared ? lh != 0 : lh >= live) continue;
-    float sum = 0.0f;
+    float all = 0.0f;
     for (int h = 0; h < (shared ? live : 1); ++h)
-      for (int w = 0; w < kGradWaves; ++w) sum += red[(w * E + e) * 64 + l + (h << a.log2_lanes)];
-    // column of (lane, e): the lane's k-th pair, side A or B, element
-    const int k = e / (2 * VW), side = (e / VW) & 1, el = e % VW;
-    const int p = (l & (L - 1)) + k * L;
-    const bool turned = p < a.rot_pairs;
-    const int ca = INTER || !turned ? 2 * p * VW : p * VW;
-    const int cb = INTER || !turned ? ca + VW : (a.rot >> 1) + p * VW;
-    const int col = (side ? cb : ca) + el;
-    if (p >= a.pairs || col >= a.head_dim) continue;
+      for (int w = 0; w < kGradWaves; ++w) all += red[(w * VW + e) * 64 + l + (h << a.log2_lanes)];
     const int global_head = (c ? a.side[0].heads : 0) + (s - a.first[c]) * hw + lh;
     const int64_t row = shared ? (int64_t)s * a.workers + blockIdx.x : (int64_t)global_head * a.workers + blockIdx.x;
-    a.partial[row * a.head_dim + col] = sum;
+    a.partial[row * a.head_dim + (l & (L - 1)) * VW + e] = all;
   }
 }
 
@@ -696,44 +597,43 @@ __global__ void __launch_bounds__(1024) qknorm_rope_grad_sum(const RopeGradArgs 
   }
 }
 
-using RopeFn = void (*)(const RopeArgs);
-using GradFn = void (*)(const RopeGradArgs);
-
 template <class IO, bool INTER, int MODE>
-RopeFn pick_rope(const RopePlan& p) {
-  if (p.piece_bytes == 16) {
-    switch (p.slots) {
-      case 1: return qknorm_rope_rows<IO, 16, 1, 1, INTER, MODE>;
-      case 2: return qknorm_rope_rows<IO, 16, 1, 2, INTER, MODE>;
-      case 3: return qknorm_rope_rows<IO, 16, 1, 3, INTER, MODE>;
-      case 4: return qknorm_rope_rows<IO, 16, 1, 4, INTER, MODE>;
-    }
-    return nullptr;
-  }
-  if (p.slots != 1) return nullptr;
-  if (p.piece_bytes == 8) return qknorm_rope_rows<IO, 8, 1, 1, INTER, MODE>;
-  if (p.np == 1) return qknorm_rope_rows<IO, IO::kBytes, 1, 1, INTER, MODE>;
-  return qknorm_rope_rows<IO, IO::kBytes, 8, 1, INTER, MODE>;
-}
-
-template <class IO>
-RopeFn pick_rope_mode(int mode, bool inter, const RopePlan& p) {
-  if (mode == ROPE_FORWARD)
-    return inter ? pick_rope<IO, true, ROPE_FORWARD>(p) : pick_rope<IO, false, ROPE_FORWARD>(p);
-  if constexpr (IO::kBytes > 1) {
-    if (mode == ROPE_APPEND_ROWS)
-      return inter ? pick_rope<IO, true, ROPE_APPEND_ROWS>(p) : pick_rope<IO, false, ROPE_APPEND_ROWS>(p);
-    return inter ? pick_rope<IO, true, ROPE_APPEND_MXFP4>(p) : pick_rope<IO, false, ROPE_APPEND_MXFP4>(p);
+const void* pick_slots(int slots) {
+  switch (slots) {
+    case 1: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 1, INTER, MODE>);
+    case 2: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 2, INTER, MODE>);
+    case 3: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 3, INTER, MODE>);
+    case 4: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 4, INTER, MODE>);
   }
   return nullptr;
 }
 
 template <class IO, bool INTER>
-GradFn pick_grad(const RopePlan& p) {
-  if (p.piece_bytes == 16) return qknorm_rope_grad<IO, 16, 1, INTER>;
-  if (p.piece_bytes == 8) return qknorm_rope_grad<IO, 8, 1, INTER>;
-  if (p.np == 1) return qknorm_rope_grad<IO, IO::kBytes, 1, INTER>;
-  return qknorm_rope_grad<IO, IO::kBytes, 8, INTER>;
+const void* pick_mode(int mode, int slots) {
+  if (mode == ROPE_FORWARD) return pick_slots<IO, INTER, ROPE_FORWARD>(slots);
+  if constexpr (IO::kBytes > 1) {
+    if (mode == ROPE_APPEND_ROWS) return pick_slots<IO, INTER, ROPE_APPEND_ROWS>(slots);
+    return pick_slots<IO, INTER, ROPE_APPEND_MXFP4>(slots);
+  }
+  return nullptr;
+}
+
+const void* rope_kernel(int mode, int dtype, bool inter, const RopePlan& p) {
+  if (!p.whole) return rope_paired_kernel(mode, dtype, inter, p);
+  switch (dtype) {
+    case kDtypeBF16: return inter ? pick_mode<BF16, true>(mode, p.slots) : pick_mode<BF16, false>(mode, p.slots);
+    case kDtypeF32: return inter ? pick_mode<F32, true>(mode, p.slots) : pick_mode<F32, false>(mode, p.slots);
+    default: return inter ? pick_mode<FP8, true>(mode, p.slots) : pick_mode<FP8, false>(mode, p.slots);
+  }
+}
+
+const void* rope_grad_kernel(int dtype, bool inter, const RopePlan& p) {
+  if (!p.whole) return rope_paired_grad_kernel(dtype, inter, p);
+  if (dtype == kDtypeBF16)
+    return inter ? reinterpret_cast<const void*>(qknorm_rope_grad<BF16, true>)
+                 : reinterpret_cast<const void*>(qknorm_rope_grad<BF16, false>);
+  return inter ? reinterpret_cast<const void*>(qknorm_rope_grad<F32, true>)
+               : reinterpret_cast<const void*>(qknorm_rope_grad<F32, false>);
 }
 
 int launched(hipError_t e, std::string* err) {
@@ -744,24 +644,48 @@ int launched(hipError_t e, std::string* err) {
 
 }  // namespace
 
-int launch_rope(int mode, int dtype, bool inter, const RopePlan& p, const RopeArgs& args, void* stream,
-                std::string* err) {
-  RopeFn fn = dtype == kDtypeBF16  ? pick_rope_mode<BF16>(mode, inter, p)
-              : dtype == kDtypeF32 ? pick_rope_mode<F32>(mode, inter, p)
-                                   : pick_rope_mode<FP8>(mode, inter, p);
+static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeArgs a, void* stream, std::string* err) {
+  const void* fn = rope_kernel(mode, dtype, inter, p);
   if (!fn) {
     *err = "no kernel compiled for this plan";
     return (int)hipErrorInvalidValue;
   }
-  const int64_t blocks = (args.T + p.tokens - 1) / p.tokens;
-  const int64_t cap = grid_cap();
-  const unsigned gy = (unsigned)((args.n_slots + p.slots * p.waves - 1) / (p.slots * p.waves));
-  RopeArgs a = args;
+  int64_t blocks = (a.T + p.tokens - 1) / p.tokens;
+  unsigned gy = 1, threads = (unsigned)(64 * p.waves * p.tokens);
+  if (p.whole) {
+    // units: waves of the first a.tokens tokens; the rest of the tokens loop
+    const int64_t most = (grid_cap() < ((int64_t)1 << 28) ? grid_cap() : (int64_t)1 << 28) * kRopeWaves / p.groups;
+    a.tokens = (int)(a.T < most ? a.T : most > 0 ? most : 1);
+    a.units = (uint32_t)((int64_t)a.tokens * p.groups);
+    a.by_groups = divisor((uint32_t)p.groups);
+    blocks = ((int64_t)a.units + kRopeWaves - 1) / kRopeWaves;
+    threads = 64 * kRopeWaves;
+  } else {
+    if (blocks > grid_cap()) blocks = grid_cap();
+    gy = (unsigned)((a.n_slots + p.slots * p.waves - 1) / (p.slots * p.waves));
+  }
   void* kargs[] = {&a};
-  return launched(hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)(blocks < cap ? blocks : cap), gy),
-                                  dim3((unsigned)(64 * p.waves * p.tokens)), kargs, 0,
+  return launched(hipLaunchKernel(fn, dim3((unsigned)blocks, gy), dim3(threads), kargs, 0,
                                   static_cast<hipStream_t>(stream)),
                   err);
+}
+
+int launch_rope(int mode, int dtype, bool inter, const RopePlan& p, const RopeArgs& args, void* stream,
+                std::string* err) {
+  if (!p.apart) return launch_rows(mode, dtype, inter, p, args, stream, err);
+  // Q by itself, in the row-type kernel (it writes rows only), then K and V
+  RopePlan part = p;
+  RopeArgs a = args;
+  a.side[1].heads = a.side[2].heads = 0;
+  a.first[2] = a.first[1];
+  part.groups = a.first[1];
+  if (const int rc = launch_rows(ROPE_APPEND_ROWS, dtype, inter, part, a, stream, err)) return rc;
+  a = args;
+  a.side[0].heads = 0;
+  a.first[1] = 0;
+  a.first[2] = args.first[2] - args.first[1];
+  part.groups = p.groups - args.first[1];
+  return launch_rows(mode, dtype, inter, part, a, stream, err);
 }
 
 int64_t rope_grad_rows(const RopeGradArgs& a) {
@@ -770,11 +694,10 @@ int64_t rope_grad_rows(const RopeGradArgs& a) {
 
 int launch_rope_grad(int dtype, bool inter, const RopePlan& p, const RopeGradArgs& args, void* stream,
                      std::string* err) {
-  GradFn fn = dtype == kDtypeBF16 ? (inter ? pick_grad<BF16, true>(p) : pick_grad<BF16, false>(p))
-                                  : (inter ? pick_grad<F32, true>(p) : pick_grad<F32, false>(p));
+  const void* fn = rope_grad_kernel(dtype, inter, p);
   RopeGradArgs a = args;
   void* kargs[] = {&a};
-  const int rc = launched(hipLaunchKernel(reinterpret_cast<const void*>(fn),
+  const int rc = launched(hipLaunchKernel(fn,
                                           dim3((unsigned)a.workers, (unsigned)a.n_slots), dim3(64 * kGradWaves), kargs,
                                           0, static_cast<hipStream_t>(stream)),
                           err);
