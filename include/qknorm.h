@@ -66,7 +66,8 @@
  * when the library first launches a kernel, caps the number of blocks per
  * launch (blocks then loop over several token groups), which leaves compute
  * units to kernels running beside these on other streams; results do not
- * depend on it.
+ * depend on it. qknorm_headwise_rope_backward and qknorm_paged_attend size
+ * their grids themselves.
  *
  * Errors
  * ------
@@ -411,8 +412,9 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
                         int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window,
                         void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that an attend call of these sizes needs (0 for sizes it
- * would reject; makes no HIP call). */
+/* Bytes of workspace that an attend call of these sizes needs, with any window
+ * (0 for sizes it would reject; makes no HIP call). max_q is 1 for a call
+ * without cu_q. */
 size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
                                      int64_t max_q, int64_t max_len);
 

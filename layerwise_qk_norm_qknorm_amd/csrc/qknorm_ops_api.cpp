@@ -3,6 +3,7 @@
 // and attention over the 4-bit cache. Plain C++ with no HIP call, as
 // qknorm_api.cpp; only the qkn::launch_* functions touch the HIP runtime.
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <string>
@@ -18,6 +19,8 @@ using namespace qkn;
 namespace {
 
 constexpr int64_t kMaxWidth = (int64_t)1 << 30;
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;          // of a sequence
+constexpr int64_t kLaunchThreads = ((int64_t)1 << 32) - 1;   // of a launch
 
 int log2_of(int64_t v) {
   int n = 0;
@@ -129,7 +132,7 @@ int slots_of(int64_t heads, const RopePlan& p) { return (int)((heads * p.lanes +
 // flight; calls of few tokens spread their slots over more waves. The waves of
 // a side take whole numbers of slots, so of the counts tried the one that
 // leaves fewest idle, of equals the largest (10 + 2 heads of 128, 16384
-// tokens: four slots 24.1 us, two 26.3).
+// tokens: three slots 24.1 us, two 26.3).
 void plan_waves(RopePlan* p, const int (&slots)[3], int64_t T) {
   const int n = slots[0] + slots[1] + slots[2];
   const auto groups = [&](int s) { return (slots[0] + s - 1) / s + (slots[1] + s - 1) / s + (slots[2] + s - 1) / s; };
@@ -384,6 +387,8 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
     slots_in[c] = slots_of(a.side[c].heads, p);
   }
   plan_waves(&p, slots_in, T);
+  if (!p.whole && slots_in[0] + slots_in[1] + slots_in[2] > 65535)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: too many heads", fn);
   p.apart = four && q && p.whole && p.slots > 1;
   a.n_slots = slots_in[0] + slots_in[1] + slots_in[2];
   const int unit = p.whole ? p.slots : 1;   // sides begin at whole waves, or at slots
@@ -539,7 +544,7 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
                              (int)(o->h / head_dim)};
     a.n_slots += slots_of(a.side[c].heads, *plan);
   }
-  if (a.n_slots > 65535)
+  if (a.n_slots > 65535 || (gstride && (wanted ? a.side[0].heads + a.side[1].heads : 0) > 65535))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: too many heads", fn);
   a.T = T;
   a.gstride = gstride;
@@ -561,9 +566,19 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
 // -------------------------------------------------------------------- attend
 // Row tiles per block and the cache's split. Rows of a sequence beyond 16 and
 // 32 take two and four row tiles (at most two at 256 columns), so that what
-// is read and widened of the cache serves more rows. The cache is split until
-// there are about `want` blocks, in chunks of at least 256 tokens.
-AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t max_q, int64_t max_len) {
+// is read and widened of the cache serves more rows.
+//
+// The cache is split so that the blocks fill one or two whole rounds of what
+// the chip holds at once (256 compute units of three or two blocks, as in the
+// kernel's launch bounds), whichever takes fewer steps of 128 tokens; a
+// block's start and end count as two steps, the joining launch as four.
+// Against splitting until there are about 1024 blocks (5 or 4 query heads to
+// a key head, 8 key heads of 128 columns): one sequence of 65536 tokens 25.5
+// -> 23.1 us, 64 of up to 8192 98 -> 90, 96 of 512 21.6 -> 11.7, 32 of 2048
+// 21.1 -> 18.0; 32 of 4096 with 4 key heads of 256 columns 35.8 -> 30.6.
+constexpr int64_t kRounds = 2, kBlockSteps = 2, kJoinSteps = 4;
+AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t max_q, int64_t max_len,
+                       int64_t window) {
   AttendPlan p;
   p.head_dim = (int)head_dim;
   const int64_t rows = max_q * group;
@@ -572,16 +587,21 @@ AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t
   p.row_tiles = (int)(tiles < 65536 ? tiles : 65536);
   p.max_q = max_q;
   const int64_t blocks = B * heads_k * p.row_tiles;
-  const int64_t want = 1024;
-  int64_t splits = blocks >= want ? 1 : (want + blocks - 1) / blocks;
-  const int64_t most = (max_len + 255) / 256;
-  p.most_splits = (int)(splits < most ? splits : most);
-  int64_t chunk = (max_len + splits - 1) / splits;
-  chunk = (chunk + 127) / 128 * 128;
-  if (chunk < 256) chunk = 256;
-  splits = (max_len + chunk - 1) / chunk;
-  p.splits = (int)splits;
-  p.chunk = (int)chunk;
+  const int64_t resident = 256 * (p.row_tile * head_dim <= 128 ? 3 : 2);
+  const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
+  p.most_splits = (int)most(max_len);
+  // what a block's rows see together, at most
+  const int64_t span = window ? std::min(max_len, window + 16 * p.row_tile / group + 33) : max_len;
+  const int64_t m = most(span);
+  int64_t least = INT64_MAX;
+  for (int64_t rounds = 0; rounds <= kRounds; ++rounds) {
+    const int64_t s = std::clamp<int64_t>(rounds * resident / blocks, 1, m);
+    int64_t chunk = ((span + s - 1) / s + 127) / 128 * 128;
+    if (chunk < 256) chunk = 256;
+    const int64_t n = (span + chunk - 1) / chunk;
+    const int64_t cost = (blocks * n + resident - 1) / resident * (chunk / 128 + kBlockSteps) + (n > 1 ? kJoinSteps : 0);
+    if (cost < least) least = cost, p.splits = (int)n, p.chunk = (int)chunk;
+  }
   return p;
 }
 
@@ -589,7 +609,7 @@ bool attend_sizes_ok(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_d
                      int64_t max_len) {
   return T >= 0 && heads_k > 0 && heads_q > 0 && heads_q % heads_k == 0 && heads_q <= 65536 &&
          (head_dim == 64 || head_dim == 128 || head_dim == 256) && B >= 0 && B <= ((int64_t)1 << 20) && max_q > 0 &&
-         max_q <= ((int64_t)1 << 30) && max_len > 0 && max_len <= ((int64_t)1 << 30);
+         max_q <= kMaxTokens && max_len > 0 && max_len <= kMaxTokens;
 }
 
 size_t attend_workspace(const AttendPlan& p, int64_t T, int64_t heads_q) {
@@ -685,8 +705,9 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   if (!batch->cu_q && T != batch->B)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: without cu_q there is one query row per sequence: T = %lld, B = %lld", fn,
                 (long long)T, (long long)batch->B);
-  if (batch->table_pages > (int64_t)INT32_MAX / cache->page_size)
-    return fail(QKNORM_ERR_UNSUPPORTED, "%s: a table row names more than 2^31 - 1 tokens", fn);
+  // positions a few tiles behind the last one still fit 32 bits
+  if (batch->table_pages > kMaxTokens / cache->page_size)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: a table row names more than 2^30 tokens", fn);
   if (batch->ld_table > INT64_MAX / 8 / (batch->B + 1))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the block table exceeds the address range", fn);
   if ((rc = check_rows(fn, "q->x", q->x, q->ld_x, q->h, T, 2))) return rc;
@@ -704,14 +725,15 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   const int64_t max_len = batch->max_len < capacity ? batch->max_len : capacity;
   if (!attend_sizes_ok(T, heads_q, cache->heads, head_dim, batch->B, max_q, max_len))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
-  AttendPlan p = plan_attend(head_dim, cache->heads, heads_q / cache->heads, batch->B, max_q, max_len);
-  if ((int64_t)batch->B * cache->heads * p.row_tiles > INT32_MAX / p.splits)
+  AttendPlan p = plan_attend(head_dim, cache->heads, heads_q / cache->heads, batch->B, max_q, max_len,
+                             window);
+  if ((int64_t)batch->B * cache->heads * p.row_tiles > kLaunchThreads / 256 / p.splits)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the launch exceeds the grid", fn);
   const size_t need = attend_workspace(p, T, heads_q);
   if (need && (!workspace || !multiple(workspace, 16) || workspace_bytes < need))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the workspace must be 16-byte aligned, at least %zu bytes", fn, need);
 
-  if (T > INT32_MAX / 2 / (heads_q / cache->heads))
+  if (T > kMaxTokens / 4 / (heads_q / cache->heads))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: T = %lld query rows are too many", fn, (long long)T);
 
   const Region y{(uintptr_t)q->y, q->ld_y, q->h, T, 2};
@@ -774,7 +796,7 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
 size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
                                      int64_t max_q, int64_t max_len) {
   if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
-  return attend_workspace(plan_attend(head_dim, heads_k, heads_q / heads_k, B, max_q < T ? max_q : T, max_len), T,
+  return attend_workspace(plan_attend(head_dim, heads_k, heads_q / heads_k, B, max_q < T ? max_q : T, max_len, 0), T,
                           heads_q);
 }
 

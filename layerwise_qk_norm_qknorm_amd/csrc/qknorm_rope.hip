@@ -644,6 +644,8 @@ int launched(hipError_t e, std::string* err) {
 
 }  // namespace
 
+constexpr int64_t kRopeMostBlocks = (int64_t)1 << 22;
+
 static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeArgs a, void* stream, std::string* err) {
   const void* fn = rope_kernel(mode, dtype, inter, p);
   if (!fn) {
@@ -654,13 +656,15 @@ static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeA
   unsigned gy = 1, threads = (unsigned)(64 * p.waves * p.tokens);
   if (p.whole) {
     // units: waves of the first a.tokens tokens; the rest of the tokens loop
-    const int64_t most = (grid_cap() < ((int64_t)1 << 28) ? grid_cap() : (int64_t)1 << 28) * kRopeWaves / p.groups;
+    // (a launch holds fewer than 2^32 threads)
+    const int64_t most = (grid_cap() < kRopeMostBlocks ? grid_cap() : kRopeMostBlocks) * kRopeWaves / p.groups;
     a.tokens = (int)(a.T < most ? a.T : most > 0 ? most : 1);
     a.units = (uint32_t)((int64_t)a.tokens * p.groups);
     a.by_groups = divisor((uint32_t)p.groups);
     blocks = ((int64_t)a.units + kRopeWaves - 1) / kRopeWaves;
     threads = 64 * kRopeWaves;
   } else {
+    if (blocks > kRopeMostBlocks) blocks = kRopeMostBlocks;
     if (blocks > grid_cap()) blocks = grid_cap();
     gy = (unsigned)((a.n_slots + p.slots * p.waves - 1) / (p.slots * p.waves));
   }

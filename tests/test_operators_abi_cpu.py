@@ -214,8 +214,10 @@ def test_append_refusals(kw, code, text):
     (dict(b=batch(cu_q=None)), INVALID, "without cu_q"),
     (dict(b=batch(block_table=None)), INVALID, "block_table"),
     (dict(b=batch(seq_lens=at(41) + 2)), INVALID, "aligned"),
-    (dict(b=batch(table_pages=1 << 30, ld_table=1 << 30)), UNSUPPORTED, "2^31"),
+    (dict(b=batch(table_pages=1 << 30, ld_table=1 << 30)), UNSUPPORTED, "2^30"),
     (dict(b=batch(B=1 << 21)), UNSUPPORTED, "limits"),
+    (dict(T=1 << 28), UNSUPPORTED, "too many"),
+    (dict(T=1 << 20, b=batch(B=1 << 20, max_q=1 << 12)), UNSUPPORTED, "grid"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=None), INVALID, "workspace"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), nb=64), INVALID, "workspace"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=at(50) + 8), INVALID, "workspace"),
