@@ -158,7 +158,7 @@ __device__ __forceinline__ Pages find_pages(const AttendArgs& a, const int32_t* 
   Pages p;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    // past the end of the sequence: its last 16 tokens again, masked later
+    // past the end of the chunk: its last 16 tokens again, masked later
     const int t = min(tok + 16 * h, last16);
     p.id[h] = load_uniform(table + (t >> a.log2_page));
   }
@@ -305,7 +305,6 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
   const int hk = pair - b * a.heads_k;
 
   const Sequence seq = sequence(a, b);
-  const int last16 = seq.len > 0 ? (seq.len - 1) & ~15 : 0;
   const int32_t* table = a.table + b * a.ld_table;
   // of this key head
   const uint64_t kc = uniform64((uint64_t)a.cache[0] + hk * a.head_stride);
@@ -370,10 +369,13 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
 
     LaneOffsets offs = lane_offsets<D>(lane);
     int q_at = lane;   // where this lane's query fragments lie in LDS
+    int last16 = 0;    // the chunk's last 16 tokens
 
     // One 32-token tile. Each part of the tile DEPTH steps on is loaded as
     // soon as the registers of this one's are free: K after the first product,
-    // V after the second. Loads past the end read the last tokens again.
+    // V after the second. Loads past the end of the chunk read its last tokens
+    // again (the next chunk's would be read from memory for nothing: one tile in
+    // seven of a 768-token chunk).
     const auto tile = [&](KTile<D>& K, VTile<D>& V, Place& at, Pages& ahead, int tok, int end) {
       // scores, transposed: lane (m, g) gets tokens 16h + 4g + i of row m
       f32x4_t s[RT][2];
@@ -558,6 +560,7 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
       const int end = min(begin + a.chunk, sp.hi);
       int tok = begin + 32 * wave;
       if (tok >= end) continue;
+      last16 = (end - 1) & ~15;
       KTile<D> K[DEPTH];
       VTile<D> V[DEPTH];
       Place at[DEPTH];
