@@ -32,7 +32,9 @@ HBM_PEAK_GBPS = 8000.0          # MI355X HBM3E, published
 ROTATE_MIN_BYTES = 1 << 30      # > 256 MB Infinity Cache + 8 x 4 MB L2
 PROFILES = os.path.join(ROOT, "profiles")
 KERNEL_SOURCES = ["layerwise_qk_norm_qknorm_amd/csrc/qknorm_kernels.hip",
+                  "layerwise_qk_norm_qknorm_amd/csrc/qknorm_device.hpp",
                   "layerwise_qk_norm_qknorm_amd/csrc/qknorm_internal.hpp",
+                  "layerwise_qk_norm_qknorm_amd/csrc/qknorm_checks.hpp",
                   "layerwise_qk_norm_qknorm_amd/csrc/qknorm_api.cpp"]
 
 
