@@ -685,16 +685,33 @@ __global__ void __launch_bounds__(256) qknorm_attend_join(const AttendArgs a, in
     const int64_t at = ((int64_t)(seq.q0 + i) * heads_q + head) * a.splits;
     const float* ml = a.part_ml + at * 2;
     const float* po = a.part_o + at * D + col;
-    float top = kNothing;
-    for (int s = grp; s < n; s += NG) top = __builtin_fmaxf(top, ml[2 * s]);
-    float l = 0.0f;
+    float top = kNothing, l = 0.0f;
     f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int s = grp; s < n; s += NG) {
-      const float ms = ml[2 * s], ls = ml[2 * s + 1];
-      const float w = __builtin_amdgcn_exp2f(ms - top);
-      l += w * ls;
-      o += *reinterpret_cast<const f32x4_t*>(po + (int64_t)s * D) * w;
+    // kAhead parts at a time, so that their loads are in flight together
+    constexpr int kAhead = 4;
+    for (int s0 = grp; s0 < n; s0 += kAhead * NG) {
+      f32x2_t sum[kAhead];
+      f32x4_t part[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = min(s0 + j * NG, n - 1);
+        sum[j] = *reinterpret_cast<const f32x2_t*>(ml + 2 * s);
+        part[j] = *reinterpret_cast<const f32x4_t*>(po + (int64_t)s * D);
+      }
+      float high = top;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) high = __builtin_fmaxf(high, sum[j][0]);
+      const float old = __builtin_amdgcn_exp2f(top - high);
+      top = high;
+      l *= old;
+      o *= old;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (s0 + j * NG >= n) break;
+        const float w = __builtin_amdgcn_exp2f(sum[j][0] - top);
+        l += w * sum[j][1];
+        o += part[j] * w;
+      }
     }
     __syncthreads();
     *reinterpret_cast<f32x4_t*>(&red[grp * D + col]) = o;
