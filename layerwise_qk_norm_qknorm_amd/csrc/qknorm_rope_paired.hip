@@ -8,6 +8,9 @@
 // lane. The head's sum of squares is a butterfly over its lanes. One pass of a
 // wave over 64 / lanes heads is a slot; slots never mix Q, K and V, so all
 // that depends on the side is scalar.
+//
+// 8192 tokens x 48 bf16 heads: of 80 columns 39.9 us (3.2 TB/s: 5 of 8 lanes
+// hold pairs), of 96 columns 42.9 (3.5 TB/s).
 
 #include "qknorm_rope_device.hpp"
 
