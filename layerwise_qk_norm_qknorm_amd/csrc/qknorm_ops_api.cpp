@@ -596,7 +596,7 @@ AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t
   const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
   p.most_splits = (int)most(max_len);
   // what a block's rows see together, at most
-  const int64_t span = window ? std::min(max_len, window + 16 * p.row_tile / group + 33) : max_len;
+  const int64_t span = window && window < max_len ? std::min(max_len, window + 16 * p.row_tile / group + 33) : max_len;
   const int64_t m = most(span);
   int64_t least = INT64_MAX;
   for (int64_t rounds = 0; rounds <= kRounds; ++rounds) {

@@ -220,6 +220,8 @@ def test_append_refusals(kw, code, text):
     (dict(T=1 << 20, b=batch(B=1 << 20, max_q=1 << 12)), UNSUPPORTED, "grid"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=None), INVALID, "workspace"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), nb=64), INVALID, "workspace"),
+    (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=None, window=(1 << 63) - 1), INVALID, "workspace"),
+    (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=None, window=8191), INVALID, "workspace"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=at(50) + 8), INVALID, "workspace"),
     (dict(b=batch(table_pages=512, ld_table=512, max_len=8192), ws=at(30)), INVALID, "overlaps"),
 ])
