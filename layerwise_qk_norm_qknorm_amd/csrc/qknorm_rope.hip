@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
 // LDS in a fixed order); qknorm_rope_grad_sum adds the rows in a fixed order,
 // so the gradients do not change from run to run. The next token's loads are
 // issued before the current one is worked on. 8192 tokens x 48 heads x 128
-// bf16 columns: 59.7 us with the sums (56 and 4), 5.1 TB/s, the rate of a large
-// copy.
+// bf16 columns: 59.7 us with the sums (57 and 5 traced one by one), 5.1 TB/s,
+// the rate of a large copy.
 template <class IO, bool INTER>
 __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGradArgs a) {
   constexpr int VW = IO::kVW;
