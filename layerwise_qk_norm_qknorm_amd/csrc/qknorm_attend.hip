@@ -82,12 +82,13 @@ __device__ __forceinline__ uint32_t widen_byte(uint32_t codes, float scale, int 
   }
 }
 
-// The larger of three; a NaN operand loses, as with fmaxf. (Through fmaxf the
-// compiler spends an instruction per operand on quieting NaNs first.)
+// The largest of three, NaN where one of them is: one v_maximum3_f32. (fmaxf
+// would spend an instruction per operand on quieting NaNs. Written as inline
+// asm it would read the scores without the wait states that a matrix product's
+// result needs, which the compiler puts only before instructions it knows.) A
+// row with a NaN score is NaN whatever its maximum.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // In a branch that few tiles take: keeps the compiler from running it for all
