@@ -99,11 +99,18 @@ def _prepared(name, args, rows, result):
     return _OperatorCall(call, rows.get_device(), result)
 
 
+def _torch_stream(stream, device):
+    """torch's stream for a stream object or handle. Handle 0 is the device's default stream
+    (ExternalStream would take it for no handle, and make a stream of its own)."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 def _at(stream, device):
     """Context in which new memory belongs to the stream a call runs on."""
-    if stream is not None and not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)     # None: no change
+    return torch.cuda.stream(None if stream is None else _torch_stream(stream, device))     # None: no change
 
 
 # ---------------------------------------------------------------- norm and rotation
