@@ -5,7 +5,11 @@ the C++ module ``_qknorm_torch``; the C names are kept).
 
 The calls run on torch's current stream of the tensors' device, whichever
 device is current, or on ``stream``. What a call allocates itself (outputs or
-a workspace that were not passed) belongs to the stream it runs on.
+a workspace that were not passed) belongs to the stream it runs on. What a
+prepared call allocates belongs to the stream that is current at its
+preparation; launches on other streams are recorded on it, so that dropping the
+call hands none of it out again while a launch still uses it. A prepared call
+that a graph has captured has to be kept as long as the graph is replayed.
 """
 
 import importlib
@@ -51,25 +55,35 @@ def rope_table(n_positions, rot_dim, base=10000.0, inv_freq=None, device="cuda")
 
 class _OperatorCall(PreparedCall):
     """A PreparedCall whose marshalled arguments the native module holds (with
-    their tensors), and that makes its tensors' device the current one."""
+    their tensors), and that makes its tensors' device the current one. `own` is
+    what was allocated for it, on the stream that is current now."""
 
-    def __init__(self, call, device, result):
+    def __init__(self, call, device, result, own=()):
         super().__init__(None, (), (), device, result)
         self._call = call
+        self._own = own
+        self._known = {_handle(device, None)}    # streams that the allocator knows to use `own`
 
     def __call__(self, stream=None):
-        _on(self._device, stream, lambda s: _native().launch(self._call, s))
+        s = _handle(self._device, stream)
+        if self._own and s not in self._known:
+            on = _torch_stream(s if stream is None else stream, torch.device("cuda", self._device))
+            for t in self._own:
+                t.record_stream(on)
+            self._known.add(s)
+        _on(self._device, s, lambda s: _native().launch(self._call, s))
         return self._result
 
 
-def _on(dev, stream, enqueue):
-    """enqueue(stream handle) with `dev` current: the default stream is the current device's own."""
+def _handle(dev, stream):
+    """The stream handle a call runs on: `stream`'s, or that of the device's current stream."""
     if stream is not None:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    elif _raw_stream is not None:
-        s = _raw_stream(dev)
-    else:
-        s = torch.cuda.current_stream(dev).cuda_stream
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _on(dev, s, enqueue):
+    """enqueue(stream handle) with `dev` current: the default stream is the current device's own."""
     if _current_device() == dev:
         rc = enqueue(s)
     else:
@@ -91,12 +105,12 @@ def _run(name, args, rows, stream):
         fn(*args, 0, True)      # raises: the rows are not on a GPU
         raise ValueError("the rows must be device tensors")
     else:
-        _on(dev, stream, lambda s: fn(*args, s, False))
+        _on(dev, _handle(dev, stream), lambda s: fn(*args, s, False))
 
 
-def _prepared(name, args, rows, result):
+def _prepared(name, args, rows, result, own=()):
     call = getattr(_native(), name)(*args, 0, True)
-    return _OperatorCall(call, rows.get_device(), result)
+    return _OperatorCall(call, rows.get_device(), result, tuple(t for t in own if t is not None))
 
 
 def _torch_stream(stream, device):
@@ -158,7 +172,7 @@ def _gradient_outputs(q, k, gamma_q, gamma_k, head_dim, stride, dx_q, dx_k, dgam
             if need_dgamma:
                 dgamma_q = _new_gradient(gamma_q, q, head_dim, stride) if dgamma_q is None else dgamma_q
                 dgamma_k = _new_gradient(gamma_k, k, head_dim, stride) if dgamma_k is None else dgamma_k
-            if workspace is None and on is not None:
+            if workspace is None and on is not None and not (dgamma_q is None and dgamma_k is None):
                 code = {torch.float32: 0, torch.bfloat16: 1}.get(q.dtype, 2)
                 need = load_library().qknorm_headwise_rope_backward_workspace(
                     q.shape[1], k.shape[1], q.shape[0], code, int(head_dim), int(stride))
@@ -190,12 +204,12 @@ def prepare_headwise_rope_backward(dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head
     """qknorm_headwise_rope_backward with its arguments checked and marshalled once
     (PreparedCall). It keeps its workspace: calls of one object must not run at the same
     time on two streams."""
-    dx_q, dx_k, dgamma_q, dgamma_k, workspace = _gradient_outputs(
-        q, k, gamma_q, gamma_k, head_dim, gamma_head_stride, dx_q, dx_k, dgamma_q, dgamma_k, need_dgamma, workspace,
-        None)
+    given = (dx_q, dx_k, dgamma_q, dgamma_k, workspace)
+    made = _gradient_outputs(q, k, gamma_q, gamma_k, head_dim, gamma_head_stride, *given[:4], need_dgamma, workspace,
+                             torch.cuda.current_stream(q.device))
     return _prepared("rope_backward", (dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions,
-                                       interleaved, gamma_head_stride, dx_q, dx_k, dgamma_q, dgamma_k, workspace), q,
-                     (dx_q, dx_k, dgamma_q, dgamma_k))
+                                       interleaved, gamma_head_stride, *made), q, made[:4],
+                     (m for m, g in zip(made, given) if g is None))
 
 
 # ---------------------------------------------------------------------- paged cache
@@ -265,6 +279,9 @@ def prepare_paged_attend(q, k_cache, v_cache, k_scales, v_scales, block_table, s
     """qknorm_paged_attend with its arguments checked and marshalled once (PreparedCall): for
     decode loops, whose seq_lens and block_table change in place between calls. It keeps its
     workspace: calls of one object must not run at the same time on two streams."""
-    out, workspace = _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace, None)
+    given = (out, workspace)
+    made = _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace,
+                          torch.cuda.current_stream(q.device))
     return _prepared("attend", (q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, head_dim, cu_q, scale,
-                                causal, window, max_q, max_len, out, workspace), q, out)
+                                causal, window, max_q, max_len, *made), q, made[0],
+                     (m for m, g in zip(made, given) if g is None))

@@ -28,3 +28,42 @@ def test_memory_for_a_stream_handle(streams):
     s = operators._at(99, dev)
     assert (s.name, s.cuda_stream) == ("external", 99)
     assert operators._at(0, dev).name == "default"          # the default stream, not a new one
+
+
+class Memory:
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, stream):
+        self.recorded.append((stream.name, stream.cuda_stream))
+
+
+def test_a_prepared_call_records_the_streams_it_runs_on(streams, monkeypatch):
+    """What was allocated for a prepared call is recorded on every other stream that the call is
+    launched on, so that the allocator waits for them before it hands the memory out again."""
+    now = {"stream": 5}
+    launched = []
+
+    class Native:
+        @staticmethod
+        def launch(call, s):
+            launched.append(s)
+            return 0
+
+    monkeypatch.setattr(operators, "_native", lambda: Native)
+    monkeypatch.setattr(operators, "_raw_stream", lambda dev: now["stream"])
+    monkeypatch.setattr(operators, "_current_device", lambda: 0)
+    memory = Memory()
+    call = operators._OperatorCall(object(), 0, "result", (memory,))
+    assert call() == "result" and memory.recorded == []        # the stream it was allocated on
+    call(stream=5)
+    assert memory.recorded == []
+    call(stream=Stream("own", 77))
+    call(stream=Stream("own", 77))                              # once a stream
+    assert memory.recorded == [("own", 77)]
+    now["stream"] = 31                                          # another current stream
+    call()
+    call(stream=0)
+    assert memory.recorded[1:] == [("external", 31), ("default", 0)]
+    assert launched == [5, 5, 77, 77, 31, 0]
+    operators._OperatorCall(object(), 0, None)(stream=77)      # nothing of its own: nothing to record
