@@ -582,17 +582,37 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
 // -> 23.1 us, 64 of up to 8192 98 -> 90, 96 of 512 21.6 -> 11.7, 32 of 2048
 // 21.1 -> 18.0; 32 of 4096 with 4 key heads of 256 columns 35.8 -> 30.6.
 constexpr int64_t kRounds = 2, kBlockSteps = 2, kJoinSteps = 4;
-AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t max_q, int64_t max_len,
-                       int64_t window) {
+
+// Blocks along the rows are meant for max_q rows of each sequence, and those
+// of shorter ones end at once, which costs 0.55 ns each. Where that asks for
+// more than 2^17 blocks (max_q left at T, or one long prompt among many
+// tokens) a sequence gets as many as fill the chip by themselves, or four
+// times its even share of the row tiles there are, and they loop over its
+// rows. 40 over 8 heads of 128: 512 sequences of 1 to 64 rows on 512 tokens,
+// max_q left at T, 3575 us -> 738 (605 with max_q = 64); 256 of 64 to 170 rows
+// 3314 -> 687 (629 with max_q = 170); 4096 rows and 511 of one row 1614 -> 1078;
+// 8192 rows and 63 of one row 2986 -> 2899, and 3174 had they been held to what
+// fills the chip there too.
+constexpr int64_t kManyBlocks = (int64_t)1 << 17;
+int64_t row_tiles_of(int64_t tiles, int64_t tile, int64_t heads_k, int64_t group, int64_t B, int64_t T,
+                     int64_t resident) {
+  const int64_t pairs = B * heads_k;
+  const int64_t fill = std::max((resident + heads_k - 1) / heads_k, kManyBlocks / pairs);
+  const int64_t even = 4 * (std::min(T, kMaxTokens) * group / tile + B) / B;
+  const int64_t most = std::max(std::min(fill, kLaunchThreads / 256 / pairs), even);
+  return std::min({tiles, most, (int64_t)65536});
+}
+AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t T, int64_t max_q,
+                       int64_t max_len, int64_t window) {
   AttendPlan p;
   p.head_dim = (int)head_dim;
   const int64_t rows = max_q * group;
   p.row_tile = rows <= 16 ? 1 : rows <= 32 || head_dim == 256 ? 2 : 4;
   const int64_t tiles = (rows + 16 * p.row_tile - 1) / (16 * p.row_tile);
-  p.row_tiles = (int)(tiles < 65536 ? tiles : 65536);
+  const int64_t resident = 256 * (p.row_tile * head_dim <= 128 ? 3 : 2);
+  p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);
   p.max_q = max_q;
   const int64_t blocks = B * heads_k * p.row_tiles;
-  const int64_t resident = 256 * (p.row_tile * head_dim <= 128 ? 3 : 2);
   const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
   p.most_splits = (int)most(max_len);
   // what a block's rows see together, at most
@@ -730,8 +750,7 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   const int64_t max_len = batch->max_len < capacity ? batch->max_len : capacity;
   if (!attend_sizes_ok(T, heads_q, cache->heads, head_dim, batch->B, max_q, max_len))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
-  AttendPlan p = plan_attend(head_dim, cache->heads, heads_q / cache->heads, batch->B, max_q, max_len,
-                             window);
+  AttendPlan p = plan_attend(head_dim, cache->heads, heads_q / cache->heads, batch->B, T, max_q, max_len, window);
   if ((int64_t)batch->B * cache->heads * p.row_tiles > kLaunchThreads / 256 / p.splits)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the launch exceeds the grid", fn);
   const size_t need = attend_workspace(p, T, heads_q);
@@ -801,8 +820,8 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
 size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
                                      int64_t max_q, int64_t max_len) {
   if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
-  return attend_workspace(plan_attend(head_dim, heads_k, heads_q / heads_k, B, max_q < T ? max_q : T, max_len, 0), T,
-                          heads_q);
+  return attend_workspace(plan_attend(head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0),
+                          T, heads_q);
 }
 
 }  // extern "C"
