@@ -359,8 +359,9 @@ typedef struct qknorm_cache {
  *   other arguments as for qknorm_headwise_rope.
  *
  * MXFP4 needs head_dim % 32 == 0. Keys bound for 4 bits are formed in float32,
- * and again in float64 where a code or a scale is near a border, so that the
- * codes are what exact arithmetic gives. No other slot of the cache is
+ * and again in float64 where a code or a scale is near a border, or a sum out
+ * of float32's range, so that the codes are what exact arithmetic gives. No
+ * other slot of the cache is
  * written. Outputs and the cache must not overlap each other or the inputs
  * (q->y == q->x in place apart); k->y and v->y may not be in place.
  */

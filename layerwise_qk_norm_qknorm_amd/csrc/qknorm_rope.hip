@@ -199,6 +199,7 @@ __device__ __forceinline__ Coded quantize(const float (&f)[VW]) {
 // The codes of values known to within kUnsure of `mag`: true if every value
 // within that distance has them (in this lane's share of its block).
 constexpr float kUnsure = 0x1p-19f;
+constexpr float kMostFactor = 0x1p24f;   // largest RMS factor for which that distance holds
 template <int VW>
 __device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float (&mag)[VW], Coded& q) {
   float lo[VW], hi[VW];
@@ -413,12 +414,14 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
       float f[VW];
       widen<IO, VW>(x[i].w, f);
       float mag[VW];
+      bool ranged = true;   // float32 held the head's sum and its products (see below)
       if (gamma) {
         float ss = 0.0f;
 #pragma unroll
         for (int e = 0; e < VW; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
         ss = group_sum(ss, L);
         const float r = rms_factor(ss, a.inv_div, a.eps);
+        ranged = r > 0.0f && r <= kMostFactor;
         float g[VW];
         widen_gamma<IO, VW>(gam.w, g);
 #pragma unroll
@@ -434,9 +437,12 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
       if (MODE == ROPE_APPEND_MXFP4 && c != 0) {
         if (c == 2) {
           q = quantize<VW>(f);
-        } else if (__builtin_amdgcn_ballot_w64(!quantize_sure<VW>(f, mag, q)) != 0) {
-          unsure |= 1u << i;
-          continue;
+        } else {
+          const bool sure = quantize_sure<VW>(f, mag, q);
+          if (__builtin_amdgcn_ballot_w64(!(sure && ranged)) != 0) {
+            unsure |= 1u << i;
+            continue;
+          }
         }
       }
       store(i, on && live, f, q, t, place);
@@ -445,10 +451,14 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
     if constexpr (MODE == ROPE_APPEND_MXFP4) {
       // A key's float32 value is within 16 u of the magnitudes it is the sum
       // of (r within 11 u: a chain of 8 squares, 6 butterfly adds, the factor;
-      // then 4 roundings), u = 2^-24; kUnsure is twice that. Where a border of
-      // the codes or of the scale lies that near to one (in about 2% of the
-      // slots) the slot is formed again in float64, so that every code is the
-      // one exact arithmetic gives and does not hang on the order of a sum.
+      // then 4 roundings), u = 2^-24; kUnsure is twice that. It is so where the
+      // sum is finite (r > 0) and subnormal roundings, of 2^-150 at most, count
+      // for nothing: with r up to 2^24 they are below u of the mean square, and
+      // below kUnsure / 16 of the lowest border there is, 2^-102. Where a border
+      // of the codes or of the scale lies that near to one (in about 2% of the
+      // slots), or r is out of that range, the slot is formed again in float64,
+      // so that every code is the one exact arithmetic gives and does not hang
+      // on the order of a sum.
       // Here, behind the others, where little else is held in registers (in
       // float64 throughout, 8192 tokens took 69 us).
 #pragma unroll 1
