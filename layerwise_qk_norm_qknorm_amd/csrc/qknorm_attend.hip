@@ -60,9 +60,10 @@ constexpr uint32_t kTopScale = 252;       // largest scale byte of a finite bloc
 // float32 sums and bf16 probabilities keep their relative accuracy at any
 // scale, and the accumulator is hardly ever rescaled.
 constexpr float kSlack = 8.0f;
-// The reference before any score: below every finite score there is, and so
-// that its differences stay finite.
-constexpr float kNothing = -1.7e38f;
+// The reference before any score: the lowest finite value, so that every score
+// that is finite in base 2 (times log2 e) counts. Differences to it may be
+// infinite, never NaN.
+constexpr float kNothing = -3.40282347e38f;
 
 struct Frag {
   uint32_t w[4];
