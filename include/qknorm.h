@@ -66,8 +66,9 @@
  * when the library first launches a kernel, caps the number of blocks per
  * launch (blocks then loop over several token groups), which leaves compute
  * units to kernels running beside these on other streams; results do not
- * depend on it. qknorm_headwise_rope_backward and qknorm_paged_attend size
- * their grids themselves.
+ * depend on it. qknorm_headwise_rope and qknorm_paged_append launch at least
+ * the blocks that one token's heads take; qknorm_headwise_rope_backward and
+ * qknorm_paged_attend size their grids themselves.
  *
  * Errors
  * ------
@@ -361,9 +362,9 @@ typedef struct qknorm_cache {
  * MXFP4 needs head_dim % 32 == 0. Keys bound for 4 bits are formed in float32,
  * and again in float64 where a code or a scale is near a border, or a sum out
  * of float32's range, so that the codes are what exact arithmetic gives. No
- * other slot of the cache is
- * written. Outputs and the cache must not overlap each other or the inputs
- * (q->y == q->x in place apart); k->y and v->y may not be in place.
+ * other slot of the cache is written. Outputs and the cache must not overlap
+ * each other or the inputs (q->y == q->x in place apart); k->y and v->y may not
+ * be in place.
  */
 int qknorm_paged_append(const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
                         int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,

@@ -682,9 +682,10 @@ static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeA
     blocks = ((int64_t)a.units + kRopeWaves - 1) / kRopeWaves;
     threads = 64 * kRopeWaves;
   } else {
-    if (blocks > kRopeMostBlocks) blocks = kRopeMostBlocks;
-    if (blocks > grid_cap()) blocks = grid_cap();
+    // gy blocks take a token's slots: the cap holds for their product, down to one token's blocks
     gy = (unsigned)((a.n_slots + p.slots * p.waves - 1) / (p.slots * p.waves));
+    const int64_t most = (grid_cap() < kRopeMostBlocks ? grid_cap() : kRopeMostBlocks) / gy;
+    if (blocks > most) blocks = most > 0 ? most : 1;
   }
   void* kargs[] = {&a};
   return launched(hipLaunchKernel(fn, dim3((unsigned)blocks, gy), dim3(threads), kargs, 0,

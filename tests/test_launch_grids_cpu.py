@@ -42,3 +42,43 @@ def test_attention_grids_that_fit_stay_as_the_bound_asks(tmp_path):
     for (T, B, q), (rc, message, launches) in zip(calls, grids([attend(*c) for c in calls], tmp_path)):
         assert rc == 0, message
         assert launches[0][0] == B * 8 * -(-q * 5 // 64), (T, B, q)
+
+
+def rope(T, heads_q, heads_k, d, dtype=1, rot=None, inter=0, **kw):
+    """A call of the rotation: packed rows, Q then K."""
+    far, ld = 1 << 52, (heads_q + heads_k) * d
+    e = 4 if dtype == 0 else 2 if dtype == 1 else 1
+    side = lambda i, h, at: ["operand", dict(i=i, h=h * d, x=far + at * e, y=2 * far + at * e, ld_x=ld, ld_y=ld)]
+    rot = d if rot is None else rot
+    return ["rope", dict(T=T, d=d, dtype=dtype, q=side(0, heads_q, 0), k=side(5, heads_k, heads_q * d),
+                         r=["rope", dict(rot_dim=rot, ld=max(rot, 1), interleaved=inter)])]
+
+
+def append(T, heads_q, heads_k, d, four=True, ps=16, dtype=1, rot=None, inter=0):
+    far, ld = 1 << 52, (heads_q + 2 * heads_k) * d
+    e = 4 if dtype == 0 else 2
+    row = lambda i, h, at, y: ["operand", dict(i=i, h=h * d, x=far + at * e, y=y, ld_x=ld, ld_y=heads_q * d)]
+    unit = d // 2 if four else d
+    c = dict(four=four, heads=heads_k, page_size=ps, n_pages=4, token_stride=unit, head_stride=ps * unit,
+             page_stride=heads_k * ps * unit)
+    if four:
+        c.update(scale_head_stride=ps * d // 32, scale_page_stride=heads_k * ps * d // 32)
+    rot = d if rot is None else rot
+    return ["append", dict(T=T, d=d, dtype=dtype, q=row(0, heads_q, 0, 2 * far), k=row(5, heads_k, heads_q * d, None),
+                           v=row(10, heads_k, (heads_q + heads_k) * d, None),
+                           r=["rope", dict(rot_dim=rot, ld=max(rot, 1), interleaved=inter)], c=["cache", c])]
+
+
+def test_the_cap_on_blocks_holds_for_the_whole_grid(tmp_path):
+    """Of both layouts (heads of 320 columns: 24 blocks' worth of waves in three blocks a token)."""
+    calls = [rope(100, 40, 8, 320), rope(5000, 40, 8, 128), rope(100, 9, 3, 81, rot=80), rope(5000, 40, 8, 80),
+             append(100, 40, 8, 320), append(5000, 10, 2, 128), append(100, 40, 8, 320, four=False),
+             append(5000, 10, 2, 128, four=False)]
+    free, capped = grids(calls, tmp_path), grids(calls, tmp_path, cap=7)
+    for call, (rc, message, launches), (_, _, most) in zip(calls, capped, free):
+        assert rc == 0, message
+        assert max(x * y for x, y, _ in most) > 7, call
+        assert max(x * y for x, y, _ in launches) <= 7, (call, launches)
+    # never less than the blocks of one token
+    rc, message, launches = grids([rope(100, 40, 8, 320)], tmp_path, cap=1)[0]
+    assert rc == 0 and launches == [[1, 3, 512]], (message, launches)
