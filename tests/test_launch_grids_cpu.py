@@ -82,3 +82,49 @@ def test_the_cap_on_blocks_holds_for_the_whole_grid(tmp_path):
     # never less than the blocks of one token
     rc, message, launches = grids([rope(100, 40, 8, 320)], tmp_path, cap=1)[0]
     assert rc == 0 and launches == [[1, 3, 512]], (message, launches)
+
+
+SIZES = {"f32": 4, "bf16": 2, "fp8": 1}
+CODES = {"f32": 0, "bf16": 1, "fp8": 2}
+
+
+def _waves(dtype, heads, d, layout, slots):
+    """Slots of each side, and the waves that a token's take."""
+    chunk = 16 // SIZES[dtype]
+    lanes = 1
+    while lanes < (d // chunk if layout == "whole" else d // (2 * chunk)):
+        lanes *= 2
+    per_side = [-(-h * lanes // 64) for h in heads]
+    if layout == "whole":
+        return sum(-(-n // slots) for n in per_side), per_side
+    return -(-sum(per_side) // slots), per_side
+
+
+def _expected(T, dtype, heads, d, layout, slots):
+    waves, _ = _waves(dtype, heads, d, layout, slots)
+    if layout == "whole":       # four waves to a block, tokens one after the other
+        return [-(-T * waves // 4), 1, 256]
+    tokens = 1 if waves >= 4 else 4 // waves
+    assert waves <= 8
+    return [-(-T // tokens), 1, 64 * waves * tokens]
+
+
+def test_the_variants_are_the_ones_that_the_gpu_tests_mean(tmp_path):
+    """operator_variants.py names the layout and slots that each of its calls takes."""
+    from operator_variants import APPEND, ROPE
+    calls, want = [], []
+    for (dtype, T, nq, nk, d, rot, inter, _, _), (layout, slots) in ROPE:
+        calls.append(rope(T, nq, nk, d, dtype=CODES[dtype], rot=rot, inter=int(inter)))
+        want.append([_expected(T, dtype, (nq, nk), d, layout, slots)])
+    for kw, (layout, slots) in APPEND:
+        T, dtype, nq, nk, d = (kw[n] for n in ("T", "dtype", "nq", "nk", "d"))
+        for four in (True, False):
+            calls.append(append(T, nq, nk, d, four=four, dtype=CODES[dtype], rot=kw["rot"], inter=int(kw["inter"])))
+            if four and layout == "whole" and slots > 1:    # Q in a launch of its own
+                want.append([_expected(T, dtype, (nq,), d, layout, slots),
+                             _expected(T, dtype, (nk, nk), d, layout, slots)])
+            else:
+                want.append([_expected(T, dtype, (nq, nk, nk), d, layout, slots)])
+    for call, launches, (rc, message, got) in zip(calls, want, grids(calls, tmp_path)):
+        assert rc == 0, message
+        assert got == launches, (call, got, launches)
