@@ -97,6 +97,14 @@ double number(PyObject* o, const char* name) {
   }
   return v;
 }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse_type(std::string(name) + " must be true or false");
+  }
+  return v != 0;
+}
 
 // ------------------------------------------------------------------- tensors
 void on_device(const at::Tensor& t, const at::Tensor& ref, const char* name) {
@@ -185,7 +193,7 @@ void rope_of(Call& c, PyObject* table, PyObject* positions, PyObject* interleave
   c.rope.rot_dim = t->size(1);
   c.rope.ld = t->size(0) > 1 ? t->stride(0) : std::max(t->stride(0), t->size(1));
   c.rope.positions = vector<int64_t>(p, c.T, at::kLong, ref, "positions");
-  c.rope.interleaved = PyObject_IsTrue(interleaved) == 1;
+  c.rope.interleaved = truth(interleaved, "interleaved");
   c.held.push_back(*t);
   c.held.push_back(p);
 }
@@ -375,7 +383,7 @@ void make_attend(Call& c, PyObject* const* a) {
   b.max_len = a[13] == Py_None ? capacity : std::min(integer(a[13], "max_len"), capacity);
   c.scale = a[9] == Py_None ? (c.head_dim > 0 ? (float)(1.0 / std::sqrt((double)c.head_dim)) : 0.0f)
                             : (float)number(a[9], "scale");
-  c.causal = PyObject_IsTrue(a[10]) == 1;
+  c.causal = truth(a[10], "causal");
   c.window = a[11] == Py_None ? 0 : integer(a[11], "window");
   c.dtype = dtype_code(q);
   size_t need = 0;
@@ -395,7 +403,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   try {
     auto call = std::make_unique<Call>();
     MAKE(*call, a);
-    if (PyObject_IsTrue(a[N + 1]) == 1) {
+    if (truth(a[N + 1], "keep")) {
       PyObject* o = PyCapsule_New(call.get(), kCapsule, drop);
       if (o) call.release();
       return o;
