@@ -289,9 +289,7 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
   constexpr int KC = D / 32;                 // 8-channel chunks a lane holds of a row
   constexpr bool QL = RT * D >= 256;         // queries in LDS, in fragment order, instead of registers
   constexpr int NP = D == 256 ? 2 : 1;       // 32-channel blocks a lane's outputs lie in
-  constexpr bool LM = true;
-  constexpr int DEPTH = 1;
-  constexpr bool LATE = RT * D >= 512;   // tiles in flight beside the current one
+  constexpr bool LATE = RT * D >= 512;       // V is loaded within its tile, after the first product: registers are short
   constexpr int kStep = 32 * kWaves;
   // the join buffer; before the join, where QL, the queries
   __shared__ __align__(16) float red[kWaves * 16 * LD];
@@ -361,16 +359,14 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
       }
     }
     if constexpr (QL) __syncthreads();
-    // The sums of the probabilities: by the same products with up to two row
-    // tiles; with four, registers are short and the lanes add their own.
-    float run_m[RT], run_l[RT];
-    f32x4_t acc[RT][CB], acc_l[LM ? RT : 1];
+    // acc_l: the sums of the probabilities, by products with a row of ones
+    float run_m[RT];
+    f32x4_t acc[RT][CB], acc_l[RT];
     uint32_t poison = 0;                  // (tile, block of channels) that NaN values reached
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       run_m[rt] = kNothing;
-      run_l[rt] = 0.0f;
-      if (LM || rt == 0) acc_l[LM ? rt : 0] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      acc_l[rt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) acc[rt][cb] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -379,11 +375,11 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
     int q_at = lane;   // where this lane's query fragments lie in LDS
     int last16 = 0;    // the chunk's last 16 tokens
 
-    // One 32-token tile. Each part of the tile DEPTH steps on is loaded as
-    // soon as the registers of this one's are free: K after the first product,
-    // V after the second. Loads past the end of the chunk read its last tokens
-    // again (the next chunk's would be read from memory for nothing: one tile in
-    // seven of a 768-token chunk).
+    // One 32-token tile. Each part of the wave's next one is loaded as soon as
+    // the registers of this one's are free: K after the first product, V after
+    // the second (LATE: this tile's V, after the first). Loads past the end of
+    // the chunk read its last tokens again (the next chunk's would be read from
+    // memory for nothing: one tile in seven of a 768-token chunk).
     const auto tile = [&](KTile<D>& K, VTile<D>& V, Place& at, Pages& ahead, int tok, int end) {
       // scores, transposed: lane (m, g) gets tokens 16h + 4g + i of row m
       f32x4_t s[RT][2];
@@ -437,10 +433,10 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
           }
       }
       if constexpr (LATE) load_v<D>(V, vc, vs, at, offs);
-      at = place_of<D>(a, ahead, tok + DEPTH * kStep, last16);
+      at = place_of<D>(a, ahead, tok + kStep, last16);
       load_k<D>(K, kc, ks, at, offs);
       // after the reads of the queries: a wait for LDS counts scalar loads too, and waits for all
-      ahead = find_pages(a, table, tok + 2 * DEPTH * kStep, last16);
+      ahead = find_pages(a, table, tok + 2 * kStep, last16);
       const bool edge = tok < lo_all || tok + 32 > min(hi_all, end);
       if (edge) {
         keep_branch();
@@ -468,16 +464,12 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
           const float nm = max3(run_m[rt], row_max(top) * a.scale_log2, run_m[rt]);
           const float alpha = __builtin_amdgcn_exp2f(run_m[rt] - nm);
           run_m[rt] = nm;
-          if constexpr (LM) acc_l[LM ? rt : 0] *= alpha;
-          run_l[rt] *= alpha;
+          acc_l[rt] *= alpha;
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) acc[rt][cb] *= alpha;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(f[j], a.scale_log2, -run_m[rt]));
-          if (!LM) run_l[rt] += f[j];
-        }
+        for (int j = 0; j < 8; ++j) f[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(f[j], a.scale_log2, -run_m[rt]));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const f32x2_t two = {f[2 * j], f[2 * j + 1]};
@@ -553,13 +545,11 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
               __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd.get(), pf[rt].get(), acc[rt][2 * p + 1], 0, 0, 0);
         }
       }
-      if constexpr (LM) {   // a row of ones for V^T: the probabilities' sums
-        const Frag ones = {{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}};
+      // a row of ones for V^T: the probabilities' sums
+      const Frag ones = {{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}};
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          acc_l[LM ? rt : 0] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones.get(), pf[rt].get(), acc_l[LM ? rt : 0], 0, 0, 0);
-      }
+      for (int rt = 0; rt < RT; ++rt)
+        acc_l[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones.get(), pf[rt].get(), acc_l[rt], 0, 0, 0);
       if (!LATE) load_v<D>(V, vc, vs, at, offs);
     };
 
@@ -569,37 +559,24 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
       int tok = begin + 32 * wave;
       if (tok >= end) continue;
       last16 = (end - 1) & ~15;
-      KTile<D> K[DEPTH];
-      VTile<D> V[DEPTH];
-      Place at[DEPTH];
-      Pages ahead[DEPTH];
-#pragma unroll
-      for (int i = 0; i < DEPTH; ++i)
-        at[i] = place_of<D>(a, find_pages(a, table, tok + i * kStep, last16), tok + i * kStep, last16);
-#pragma unroll
-      for (int i = 0; i < DEPTH; ++i) {
-        ahead[i] = find_pages(a, table, tok + (DEPTH + i) * kStep, last16);
-        // in the order in which the loop issues and awaits them: its waits
-        // count the loads behind the one they are for, and hold for both
-        __builtin_amdgcn_sched_barrier(0);
-        load_k<D>(K[i], kc, ks, at[i], offs);
-        __builtin_amdgcn_sched_barrier(0);
-        if (!LATE) load_v<D>(V[i], vc, vs, at[i], offs);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // every step works all DEPTH tiles; one past the end of the chunk is
-      // masked whole (a branch around it would make the waits for the loads
-      // hold for both ways, and so wait for all)
-      for (; tok < end; tok += DEPTH * kStep) {
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) tile(K[i], V[i], at[i], ahead[i], tok + i * kStep, end);
-      }
+      KTile<D> K;
+      VTile<D> V;
+      Place at = place_of<D>(a, find_pages(a, table, tok, last16), tok, last16);
+      Pages ahead = find_pages(a, table, tok + kStep, last16);
+      // in the order in which the loop issues and awaits them: its waits
+      // count the loads behind the one they are for, and hold for both
+      __builtin_amdgcn_sched_barrier(0);
+      load_k<D>(K, kc, ks, at, offs);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!LATE) load_v<D>(V, vc, vs, at, offs);
+      __builtin_amdgcn_sched_barrier(0);
+      for (; tok < end; tok += kStep) tile(K, V, at, ahead, tok, end);
     }
 
     // Join the four waves: one row tile at a time through LDS.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float sum = LM ? acc_l[LM ? rt : 0][0] : swap_add32(swap_add16(run_l[rt]));
+      const float sum = acc_l[rt][0];
       __syncthreads();   // the buffer's last readers are done
       if (g == 0) {
         red_m[wave * 16 + m] = run_m[rt];
