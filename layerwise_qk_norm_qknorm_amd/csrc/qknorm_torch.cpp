@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <memory>
 #include <string>
@@ -198,6 +199,14 @@ void rope_of(Call& c, PyObject* table, PyObject* positions, PyObject* interleave
   c.held.push_back(p);
 }
 
+// Strides of a cache's pages, heads and tokens. An axis of length one may carry
+// any: what a packed axis would have is taken.
+void strides_of(const at::Tensor& t, int64_t inner, int64_t (&s)[3]) {
+  s[2] = t.size(2) == 1 ? inner : t.stride(2);
+  s[1] = t.size(1) == 1 ? s[2] * t.size(2) : t.stride(1);
+  s[0] = t.size(0) == 1 ? std::max(s[1] * t.size(1), s[2] * t.size(2)) : t.stride(0);
+}
+
 // A cache of [pages, heads, page_size, head_dim] tensors (any strides, a
 // head's row contiguous), or of uint8 codes [.., head_dim / 2] with uint8
 // scales [.., head_dim / 32].
@@ -216,7 +225,10 @@ void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs,
     on_device(*t, ref, "the cache");
     c.held.push_back(*t);
   }
-  if (k.sizes() != v.sizes() || k.strides() != v.strides())
+  int64_t s[3], sv[3];
+  strides_of(k, last, s);
+  strides_of(v, last, sv);
+  if (k.sizes() != v.sizes() || !std::equal(s, s + 3, sv))
     refuse("k_cache and v_cache must have the same shape and strides");
   qknorm_cache_t& o = c.cache;
   o.format = four ? QKNORM_CACHE_MXFP4 : QKNORM_CACHE_ROWS;
@@ -225,14 +237,6 @@ void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs,
   o.n_pages = k.size(0);
   o.heads = k.size(1);
   o.page_size = k.size(2);
-  // an axis of length one may carry any stride: what it would hold is a valid one
-  const auto strides = [](const at::Tensor& t, int64_t inner, int64_t s[3]) {
-    s[2] = t.size(2) == 1 ? inner : t.stride(2);
-    s[1] = t.size(1) == 1 ? std::max(t.stride(1), s[2] * t.size(2)) : t.stride(1);
-    s[0] = t.size(0) == 1 ? std::max(t.stride(0), std::max(s[1] * t.size(1), s[2] * t.size(2))) : t.stride(0);
-  };
-  int64_t s[3];
-  strides(k, last, s);
   o.page_stride = s[0];
   o.head_stride = s[1];
   o.token_stride = s[2];
@@ -247,10 +251,11 @@ void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs,
     on_device(*t, ref, "the scales");
     c.held.push_back(*t);
   }
-  if (ks->strides() != vs->strides()) refuse("k_scales and v_scales must have the same strides");
+  strides_of(*ks, blocks, s);
+  strides_of(*vs, blocks, sv);
+  if (!std::equal(s, s + 3, sv)) refuse("k_scales and v_scales must have the same strides");
   o.k_scales = ks->data_ptr();
   o.v_scales = vs->data_ptr();
-  strides(*ks, blocks, s);
   o.scale_page_stride = s[0];
   o.scale_head_stride = s[1];
 }
