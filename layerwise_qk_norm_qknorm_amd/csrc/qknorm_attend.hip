@@ -30,13 +30,16 @@
 // that a lane's codes are 16 (K) and 4 (V) consecutive bytes at 128 channels.
 //
 // What bounds it. Decoding with many blocks: the cache's bytes (64 sequences of
-// up to 8192 tokens, 8 key heads of 128 columns: 88.9 us with the joining
-// launch, 4.6 TB/s, the rate of a large copy). One long sequence: each wave's
-// chain of a few tiles and the second launch (65536 tokens 22.2 us, 17 + 5;
-// 3.2 TB/s). Prompts: 1024 rows a sequence on 8192 tokens, four of them, take
-// 650 us, 735 TFLOP/s; the matrix unit is busy for 203 us of it and the vector
-// unit (widening, exponentials, masks) for 280, and two waves per SIMD, all
-// that the accumulators leave room for, overlap the two only in part.
+// up to 8192 tokens, 8 key heads of 128 columns: 88.8 us, 83 of them in this
+// launch at 4.95 TB/s, where a copy reaches 6.06). One long sequence: each
+// wave's chain of a few tiles and the second launch (65536 tokens 21.9 us, 17 +
+// 5; 3.3 TB/s). Prompts: 1024 rows a sequence on 8192 tokens, four of them, take
+// 644 us, 740 TFLOP/s. The matrix unit is busy for 203 us of it and the vector
+// unit (widening, exponentials, masks) for 275, and two waves per SIMD are all
+// that the accumulators leave room for; at least 166 us are neither: the blocks
+// are 4.3 rounds of what the chip holds (the last round costs 15% by their
+// lengths alone), the rest waits. Two of 1024 rows on 4096 tokens: 32 heads of 64
+// columns 100 us (466 TFLOP/s), 16 of 256 161 (578).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

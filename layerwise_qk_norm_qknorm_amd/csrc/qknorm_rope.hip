@@ -18,8 +18,8 @@
 // (rot/2 columns), a DPP move inside a 16-lane row and a permlane swap across
 // rows. The first layout tried kept both members of a pair in one lane, which
 // needs no exchange but reads a head in two 128-byte runs per instruction.
-// 8192 tokens x 48 heads x 128 bf16 columns: half-split 39.0 -> 37.0 us (5.6
-// TB/s), interleaved 45 -> 36.6, no rotation 43 -> 36; gradients 79 -> 59.
+// 8192 tokens x 48 heads x 128 bf16 columns: half-split 39.0 -> 36.6 us (5.6
+// TB/s; float32 71.5, 5.7 TB/s; FP8 35.7, bound by its conversions), interleaved 45 -> 36.6, no rotation 43 -> 36; gradients 79 -> 59.
 // Slots never mix Q, K and V, so all that depends on the side is scalar. Other
 // heads take the layout of qknorm_rope_paired.hip.
 
@@ -320,9 +320,10 @@ __device__ __forceinline__ void coded_values(const Coded& q, float (&f)[VW]) {
 // slots of one side; which, its number says (a.groups waves per token). All of
 // a wave's rows are loaded before the first is used, and the angles serve all
 // its slots.
-// 8192 tokens of 40 + 8 + 8 bf16 heads of 128 into a 4-bit cache: 60 us, 4.1
-// TB/s; Q's launch 33 us runs at the rate of a copy, K's and V's 27 us is bound
-// by the quantisation (490 vector instructions a wave, 64% of the cycles).
+// 8192 tokens of 40 + 8 + 8 bf16 heads of 128 into a 4-bit cache: 60.4 us, 4.1
+// TB/s, 58.1 without the cached values as rows; Q's launch 33 us runs at 5.1
+// TB/s, K's and V's 27 us is bound by the quantisation (504 vector instructions
+// a wave, 65% of the cycles). Into a cache of bf16 rows 42.0 us, 5.7 TB/s.
 // Apart, because one kernel for both took the registers of the longer one:
 // 70 us. The paired layout is faster only for a cache of rows and about a
 // thousand tokens (10.7 us against 11.7).
@@ -487,8 +488,8 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
 // LDS in a fixed order); qknorm_rope_grad_sum adds the rows in a fixed order,
 // so the gradients do not change from run to run. The next token's loads are
 // issued before the current one is worked on. 8192 tokens x 48 heads x 128
-// bf16 columns: 59.7 us with the sums (57 and 5 traced one by one), 5.1 TB/s,
-// the rate of a large copy.
+// bf16 columns: 59.5 us with the sums (56 and 5 traced one by one), 5.1 TB/s
+// where a copy of one stream reaches 6.06; 32 float32 heads 72.9 us, 5.6 TB/s.
 template <class IO, bool INTER>
 __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGradArgs a) {
   constexpr int VW = IO::kVW;

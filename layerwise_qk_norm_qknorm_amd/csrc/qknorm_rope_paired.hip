@@ -9,8 +9,10 @@
 // wave over 64 / lanes heads is a slot; slots never mix Q, K and V, so all
 // that depends on the side is scalar.
 //
-// 8192 tokens x 48 bf16 heads: of 80 columns 39.9 us (3.2 TB/s: 5 of 8 lanes
-// hold pairs), of 96 columns 42.9 (3.5 TB/s).
+// 8192 tokens x 48 bf16 heads: of 80 columns 40.8 us (3.2 TB/s: 5 of 8 lanes
+// hold pairs), of 96 columns 43.1 (3.6 TB/s); their gradients 49.7 and 59.6 (3.9
+// TB/s); 40 + 8 + 8 heads of 96 into a 4-bit cache 71.3 (2.3 TB/s: every key in
+// float64).
 
 #include "qknorm_rope_device.hpp"
 
