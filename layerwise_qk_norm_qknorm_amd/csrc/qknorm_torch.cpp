@@ -265,7 +265,7 @@ void workspace_of(Call& c, PyObject* given, size_t need, const at::Tensor& ref) 
   if (!t) {
     if (!need) return;
     // from the caching allocator, on the device's current stream: the callers
-    // that name another stream pass memory of that stream
+    // that name another stream, or keep the call, pass memory of their own
     c.held.push_back(at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(ref.device())));
     t = &c.held.back();
   } else {

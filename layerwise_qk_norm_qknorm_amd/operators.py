@@ -122,6 +122,11 @@ def _torch_stream(stream, device):
     return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
 
 
+def _current(rows):
+    """The current stream of rows' device (None: not on a GPU, which the native module refuses)."""
+    return torch.cuda.current_stream(rows.device) if rows.is_cuda else None
+
+
 def _at(stream, device):
     """Context in which new memory belongs to the stream a call runs on."""
     return torch.cuda.stream(None if stream is None else _torch_stream(stream, device))     # None: no change
@@ -206,7 +211,7 @@ def prepare_headwise_rope_backward(dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head
     time on two streams."""
     given = (dx_q, dx_k, dgamma_q, dgamma_k, workspace)
     made = _gradient_outputs(q, k, gamma_q, gamma_k, head_dim, gamma_head_stride, *given[:4], need_dgamma, workspace,
-                             torch.cuda.current_stream(q.device))
+                             _current(q))
     return _prepared("rope_backward", (dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions,
                                        interleaved, gamma_head_stride, *made), q, made[:4],
                      (m for m, g in zip(made, given) if g is None))
@@ -281,7 +286,7 @@ def prepare_paged_attend(q, k_cache, v_cache, k_scales, v_scales, block_table, s
     workspace: calls of one object must not run at the same time on two streams."""
     given = (out, workspace)
     made = _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace,
-                          torch.cuda.current_stream(q.device))
+                          _current(q))
     return _prepared("attend", (q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, head_dim, cu_q, scale,
                                 causal, window, max_q, max_len, *made), q, made[0],
                      (m for m, g in zip(made, given) if g is None))

@@ -1,9 +1,12 @@
 """Which stream's memory the operators' Python calls take, without a GPU: torch's
 stream functions are replaced by records of what is asked of them."""
 
+import os
+
 import pytest
 import torch
 
+import layerwise_qk_norm_qknorm_amd as qk
 from layerwise_qk_norm_qknorm_amd import operators
 
 
@@ -67,3 +70,16 @@ def test_a_prepared_call_records_the_streams_it_runs_on(streams, monkeypatch):
     assert memory.recorded[1:] == [("external", 31), ("default", 0)]
     assert launched == [5, 5, 77, 77, 31, 0]
     operators._OperatorCall(object(), 0, None)(stream=77)      # nothing of its own: nothing to record
+
+
+@pytest.mark.skipif(not os.path.exists(qk.library_path()),
+                    reason="libqknorm.so not built (run __graft_entry__.build())")
+def test_prepared_calls_refuse_tensors_that_are_not_on_a_gpu():
+    q, k = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16)
+    g = torch.ones(128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device tensor"):
+        qk.prepare_headwise_rope_backward(q, k, q, k, g, g, 1e-6, 128, None, None)
+    cache = [torch.zeros(2, 1, 16, n, dtype=torch.uint8) for n in (64, 64, 4, 4)]
+    one = torch.ones(4, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device tensor"):
+        qk.prepare_paged_attend(q, *cache, one, one[:, 0].contiguous(), 128)
