@@ -66,9 +66,9 @@
  * when the library first launches a kernel, caps the number of blocks per
  * launch (blocks then loop over several token groups), which leaves compute
  * units to kernels running beside these on other streams; results do not
- * depend on it. qknorm_headwise_rope and qknorm_paged_append launch at least
- * the blocks that one token's heads take; qknorm_headwise_rope_backward and
- * qknorm_paged_attend size their grids themselves.
+ * depend on it. qknorm_headwise_rope, qknorm_paged_append (with several axes too)
+ * and qknorm_paged_gather launch at least the blocks that one token's heads take;
+ * the gradients and the attention size their grids themselves.
  *
  * Errors
  * ------
@@ -224,7 +224,7 @@ int qknorm_headwise(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_
 
 /* ------------------------------------------------------------------------
  * Headwise QK-Norm with the position rotation, its gradients, appending to a
- * paged cache, and attention over a 4-bit cache.
+ * paged cache, reading it back, and attention over it.
  *
  * The rotation (rotary position embedding) turns each pair (a, b) of a head's
  * first rot_dim columns by its position's angle: (a c - b s, b c + a s). The
@@ -262,6 +262,33 @@ typedef struct qknorm_rope {
 int qknorm_headwise_rope(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype,
                          float eps, int64_t head_dim, int64_t gamma_head_stride,
                          const qknorm_rope_t* rope, void* stream);
+
+/* Most axes of positions. */
+#define QKNORM_MAX_AXES 4
+
+/* Positions on several axes (images and video: time, height, width): each angle
+ * takes the position of one of them. */
+typedef struct qknorm_axes {
+  int n_axes;                /* in [1, QKNORM_MAX_AXES] */
+  const uint8_t* axis;       /* host memory, [rot_dim / 2]: the axis of every angle, below n_axes. Read during
+                                the call only. */
+  int64_t ld_positions;      /* rope->positions is [n_axes][T] with this row stride in elements, >= 0 (0: the
+                                axes share one row) */
+} qknorm_axes_t;
+
+/*
+ * qknorm_headwise_rope_axes -- qknorm_headwise_rope with positions on several
+ * axes: angle i of token t is that of position rope->positions[axis[i] *
+ * ld_positions + t]. A position outside the table makes the columns that its
+ * axis turns NaN.
+ *
+ *   axes  (host pointer); NULL: one axis, as qknorm_headwise_rope. Not used with
+ *         rot_dim = 0.
+ *   other arguments as for qknorm_headwise_rope.
+ */
+int qknorm_headwise_rope_axes(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype, float eps,
+                              int64_t head_dim, int64_t gamma_head_stride, const qknorm_rope_t* rope,
+                              const qknorm_axes_t* axes, void* stream);
 
 /* One of Q or K of the backward pass. */
 typedef struct qknorm_grad_operand {
@@ -305,22 +332,34 @@ int qknorm_headwise_rope_backward(const qknorm_grad_operand_t* q, const qknorm_g
 size_t qknorm_headwise_rope_backward_workspace(int64_t hq, int64_t hk, int64_t T, int dtype, int64_t head_dim,
                                                int64_t gamma_head_stride);
 
+/* qknorm_headwise_rope_axes_backward -- gradients of qknorm_headwise_rope_axes, as
+ * qknorm_headwise_rope_backward gives those of qknorm_headwise_rope (with its workspace). */
+int qknorm_headwise_rope_axes_backward(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T,
+                                       int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                                       const qknorm_rope_t* rope, const qknorm_axes_t* axes, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
 typedef enum qknorm_cache_format {
   QKNORM_CACHE_ROWS = 0,  /* elements of the row type */
-  QKNORM_CACHE_MXFP4 = 1  /* 4 bits an element: E2M1 codes (0 .5 1 1.5 2 3 4 6 and their negatives;
+  QKNORM_CACHE_MXFP4 = 1, /* 4 bits an element: E2M1 codes (0 .5 1 1.5 2 3 4 6 and their negatives;
                              an even channel in its byte's low half) and one E8M0 scale byte (2^(byte - 127))
                              per 32 channels of a head. Written blocks take E = floor(log2(largest
                              magnitude)) - 2, held to [-100, 125], codes rounded to nearest even and
                              saturated at 6. A block that held an infinity or NaN gets the byte 255; bytes
                              above 252 read as NaN. */
+  QKNORM_CACHE_MXFP8 = 3  /* 8 bits an element: E4M3 codes (bias 7, max 448, 0x7F and 0xFF NaN) and one E8M0
+                             scale byte per 32 channels of a head. Written blocks take E = floor(log2(largest
+                             magnitude)) - 8, held to [-100, 119], codes rounded to nearest even and
+                             saturated at 448. A block that held an infinity or NaN gets the byte 255; bytes
+                             above 246 read as NaN. */
 } qknorm_cache_format_t;
 
 /*
  * A paged cache of keys and values. Token `slot % page_size` of page `slot /
  * page_size` and key head h begins at
  *     k + page * page_stride + h * head_stride + token * token_stride
- * (elements of the row type, or bytes for MXFP4), head_dim consecutive elements
- * (head_dim / 2 bytes); its scales at
+ * (elements of the row type, or bytes for MXFP4 and MXFP8), head_dim consecutive
+ * elements (head_dim / 2 or head_dim bytes); its scales at
  *     k_scales + page * scale_page_stride + h * scale_head_stride + token * head_dim / 32
  * (bytes). v is laid out alike.
  */
@@ -328,15 +367,15 @@ typedef struct qknorm_cache {
   int format;              /* qknorm_cache_format_t */
   void* k;
   void* v;
-  void* k_scales;          /* MXFP4 only, as are the two strides below */
+  void* k_scales;          /* MXFP4 and MXFP8 only, as are the two strides below */
   void* v_scales;
-  int64_t page_stride;     /* MXFP4: multiples of 16, and k and v 16-byte aligned */
+  int64_t page_stride;     /* MXFP4, MXFP8: multiples of 16, and k and v 16-byte aligned */
   int64_t head_stride;
-  int64_t token_stride;    /* MXFP4: head_dim / 2 (a head's tokens are packed) */
+  int64_t token_stride;    /* MXFP4: head_dim / 2 (a head's tokens are packed); MXFP8: a multiple of 16 */
   int64_t scale_page_stride;   /* multiples of 16, and the scales 16-byte aligned */
   int64_t scale_head_stride;
   int64_t n_pages;         /* > 0 */
-  int64_t page_size;       /* tokens, a power of two; MXFP4: at least 16 */
+  int64_t page_size;       /* tokens, a power of two; MXFP4, MXFP8: at least 16 */
   int64_t heads;           /* key heads */
 } qknorm_cache_t;
 
@@ -359,7 +398,7 @@ typedef struct qknorm_cache {
  *   dtype  QKNORM_F32 or QKNORM_BF16
  *   other arguments as for qknorm_headwise_rope.
  *
- * MXFP4 needs head_dim % 32 == 0. Keys bound for 4 bits are formed in float32,
+ * MXFP4 and MXFP8 need head_dim % 32 == 0. Keys bound for codes are formed in float32,
  * and again in float64 where a code or a scale is near a border, or a sum out
  * of float32's range, so that the codes are what exact arithmetic gives. No
  * other slot of the cache is written. Outputs and the cache must not overlap
@@ -370,7 +409,34 @@ int qknorm_paged_append(const qknorm_operand_t* q, const qknorm_operand_t* k, co
                         int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
                         const qknorm_rope_t* rope, const qknorm_cache_t* cache, const int64_t* slots, void* stream);
 
-/* The batch that qknorm_paged_attend works on. All arrays are device memory. */
+/* qknorm_paged_append_axes -- qknorm_paged_append with positions on several axes
+ * (axes as for qknorm_headwise_rope_axes). */
+int qknorm_paged_append_axes(const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
+                             int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                             const qknorm_rope_t* rope, const qknorm_axes_t* axes, const qknorm_cache_t* cache,
+                             const int64_t* slots, void* stream);
+
+/*
+ * qknorm_paged_gather -- reads a paged cache back: row t of k_rows and v_rows gets
+ * the keys and values that slot slots[t] holds, heads side by side, in the row
+ * type. The inverse of qknorm_paged_append for a prefix that is to be used
+ * elsewhere (another layout, another device, an exact product).
+ *
+ *   cache   any format. QKNORM_CACHE_ROWS: elements of `dtype`, copied as they are.
+ *   slots   device int64 [T], as in qknorm_paged_append: a negative slot, or one past
+ *           the last page, leaves its row as it was. The same slot may occur more than
+ *           once.
+ *   dtype   QKNORM_F32 or QKNORM_BF16: the type of the rows written. Codes are widened
+ *           exactly where their value fits it (bf16: all values of at least 2^-133).
+ *   k_rows, ld_k, v_rows, ld_v  row strides in elements, >= cache->heads * head_dim;
+ *           one of them may be NULL (not wanted). They must not overlap each other or
+ *           the cache.
+ *   head_dim <= QKNORM_MAX_ROPE_HEAD, a multiple of 32 for MXFP4 and MXFP8.
+ */
+int qknorm_paged_gather(const qknorm_cache_t* cache, int64_t head_dim, const int64_t* slots, int64_t T, int dtype,
+                        void* k_rows, int64_t ld_k, void* v_rows, int64_t ld_v, void* stream);
+
+/* The batch that the attention calls work on. All arrays are device memory. */
 typedef struct qknorm_batch {
   const int32_t* block_table;  /* [B][table_pages]: page ids in sequence order; row stride ld_table.
                                   An id outside [0, n_pages) among a sequence's tokens makes the rows
@@ -419,6 +485,32 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
  * without cu_q. */
 size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
                                      int64_t max_q, int64_t max_len);
+
+/*
+ * qknorm_paged_attend_wide -- qknorm_paged_attend over a cache of bf16 rows or
+ * MXFP8: prompts, chunks of new tokens behind what the cache holds, and single
+ * tokens.
+ *
+ *   cache      format QKNORM_CACHE_ROWS (of bf16) or QKNORM_CACHE_MXFP8; pages of at
+ *              least 16 tokens; 16-byte aligned pointers, and page, head and token
+ *              strides multiples of 16 bytes, a head's tokens less than 4 GiB / 16 apart
+ *   workspace  at least qknorm_paged_attend_wide_workspace(...) bytes, as there
+ *   other arguments as for qknorm_paged_attend.
+ *
+ * Scores, softmax statistics and sums are float32; probabilities are rounded to
+ * bf16 for the second product (their sums are of the rounded ones), the result once
+ * more. An infinity or NaN of a cached token reaches only the rows that see the
+ * token: a NaN of K makes the whole row NaN, one of V its column; an infinite value
+ * gives an infinity, or NaN where its probability vanishes in float32.
+ */
+int qknorm_paged_attend_wide(const qknorm_operand_t* q, int64_t T, int dtype, const qknorm_cache_t* cache,
+                             int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that such a call needs, with any window (0 for sizes it
+ * would reject; makes no HIP call). max_q is 1 for a call without cu_q. */
+size_t qknorm_paged_attend_wide_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
+                                          int64_t max_q, int64_t max_len);
 
 /* Message for the last non-OK return on the calling thread ("" if none). */
 const char* qknorm_last_error(void);

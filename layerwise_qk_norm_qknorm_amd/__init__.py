@@ -23,9 +23,12 @@ from .binding import (  # noqa: F401
     prepare_partial_stats,
 )
 
-_OPERATORS = ("prepare_headwise_rope", "prepare_headwise_rope_backward", "prepare_paged_append",
-              "prepare_paged_attend", "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "qknorm_paged_append",
-              "qknorm_paged_attend", "rope_table")
+_OPERATORS = ("prepare_headwise_rope", "prepare_headwise_rope_axes", "prepare_headwise_rope_axes_backward",
+              "prepare_headwise_rope_backward", "prepare_paged_append", "prepare_paged_append_axes",
+              "prepare_paged_attend", "prepare_paged_attend_wide", "prepare_paged_gather", "qknorm_headwise_rope",
+              "qknorm_headwise_rope_axes", "qknorm_headwise_rope_axes_backward", "qknorm_headwise_rope_backward",
+              "qknorm_paged_append", "qknorm_paged_append_axes", "qknorm_paged_attend", "qknorm_paged_attend_wide",
+              "qknorm_paged_gather", "rope_axes", "rope_table")
 
 
 def __getattr__(name):

@@ -28,8 +28,10 @@ ABI_VERSION = 3
 EXPORTS = ("qknorm_fused", "qknorm_partial_stats", "qknorm_apply_with_stats", "qknorm_headwise",
            "qknorm_last_error", "qknorm_abi_version", "qknorm_describe_plan", "qknorm_describe_headwise_plan",
            "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "qknorm_headwise_rope_backward_workspace",
-           "qknorm_paged_append", "qknorm_paged_attend", "qknorm_paged_attend_workspace")
-CACHE_ROWS, CACHE_MXFP4 = 0, 1
+           "qknorm_paged_append", "qknorm_paged_attend", "qknorm_paged_attend_workspace",
+           "qknorm_headwise_rope_axes", "qknorm_headwise_rope_axes_backward", "qknorm_paged_append_axes",
+           "qknorm_paged_gather", "qknorm_paged_attend_wide", "qknorm_paged_attend_wide_workspace")
+CACHE_ROWS, CACHE_MXFP4, CACHE_MXFP8 = 0, 1, 3
 
 
 _DTYPES = {"f32": (QKNORM_F32, 4), "bf16": (QKNORM_BF16, 2), "fp8": (QKNORM_FP8_E4M3, 1)}
@@ -66,6 +68,16 @@ class Rope(ctypes.Structure):
         ("positions", ctypes.c_void_p),
         ("rot_dim", ctypes.c_int64),
         ("interleaved", ctypes.c_int),
+    ]
+
+
+class Axes(ctypes.Structure):
+    """qknorm_axes_t."""
+
+    _fields_ = [
+        ("n_axes", ctypes.c_int),
+        ("axis", ctypes.c_char_p),
+        ("ld_positions", ctypes.c_int64),
     ]
 
 
@@ -151,7 +163,8 @@ def load_library():
         for fn in ("qknorm_fused", "qknorm_partial_stats", "qknorm_apply_with_stats", "qknorm_headwise",
                    "qknorm_describe_plan", "qknorm_describe_headwise_plan", "qknorm_abi_version",
                    "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "qknorm_paged_append",
-                   "qknorm_paged_attend"):
+                   "qknorm_paged_attend", "qknorm_headwise_rope_axes", "qknorm_headwise_rope_axes_backward",
+                   "qknorm_paged_append_axes", "qknorm_paged_gather", "qknorm_paged_attend_wide"):
             getattr(lib, fn).restype = ci
         R, G, C, B, sz = (ctypes.POINTER(Rope), ctypes.POINTER(GradOperand), ctypes.POINTER(Cache),
                           ctypes.POINTER(Batch), ctypes.c_size_t)
@@ -163,6 +176,14 @@ def load_library():
         lib.qknorm_paged_attend.argtypes = [P, i64, ci, C, i64, B, fl, ci, i64, vp, sz, vp]
         lib.qknorm_paged_attend_workspace.argtypes = [i64] * 7
         lib.qknorm_paged_attend_workspace.restype = sz
+        A = ctypes.POINTER(Axes)
+        lib.qknorm_headwise_rope_axes.argtypes = [P, P, i64, ci, fl, i64, i64, R, A, vp]
+        lib.qknorm_headwise_rope_axes_backward.argtypes = [G, G, i64, ci, fl, i64, i64, R, A, vp, sz, vp]
+        lib.qknorm_paged_append_axes.argtypes = [P, P, P, i64, ci, fl, i64, i64, R, A, C, vp, vp]
+        lib.qknorm_paged_gather.argtypes = [C, i64, vp, i64, ci, vp, i64, vp, i64, vp]
+        lib.qknorm_paged_attend_wide.argtypes = lib.qknorm_paged_attend.argtypes
+        lib.qknorm_paged_attend_wide_workspace.argtypes = [i64] * 7
+        lib.qknorm_paged_attend_wide_workspace.restype = sz
         lib.qknorm_last_error.restype = ctypes.c_char_p
         lib.qknorm_last_error.argtypes = []
         lib.qknorm_abi_version.argtypes = []

@@ -13,10 +13,12 @@ file, where the binding (``libqknorm.so``) and bench.py (the others) load
 them from.
 """
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,11 +30,12 @@ CLOCKS_LIB = os.path.join(PKG, "libqknorm_clocks.so")
 CEIL_CLOCKS_LIB = os.path.join(PKG, "libstreamceil_clocks.so")
 
 SOURCES = ["qknorm_api.cpp", "qknorm_ops_api.cpp", "qknorm_kernels.hip", "qknorm_rope.hip",
-           "qknorm_rope_paired.hip", "qknorm_attend.hip"]
+           "qknorm_rope_paired.hip", "qknorm_attend.hip", "qknorm_attend_wide.hip", "qknorm_gather.hip"]
 CEIL_SOURCES = ["stream_ceiling.hip"]
 TORCH_LIB = os.path.join(PKG, "_qknorm_torch.so")
 TORCH_SOURCE = os.path.join(CSRC, "qknorm_torch.cpp")
 ARCH = "gfx950"
+JOBS = 6       # compilers at a time, 1 to 3 GB each
 
 
 def hipcc():
@@ -42,9 +45,12 @@ def hipcc():
     raise RuntimeError("hipcc not found (ROCm is required to build libqknorm.so)")
 
 
-def command(out, sources=SOURCES, defines=()):
+def command(out, sources, defines=(), link=False):
+    """hipcc of the sources into an object, or of objects into a library."""
+    if link:
+        return [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *sources, "-o", out]
     return [
-        hipcc(), "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-shared",
+        hipcc(), "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-c",
         "-Wall", "-Wno-unused-function", *[f"-D{d}" for d in defines],
         # Packed fp32 instructions stay off: the compiler would form them
         # from plain float code, and they are not used anywhere here.
@@ -55,29 +61,16 @@ def command(out, sources=SOURCES, defines=()):
     ]
 
 
-def _start(lib, sources, defines, verbose):
-    tmp = lib + ".tmp"
-    cmd = command(tmp, sources, defines)
+def _run(cmd, verbose):
     if verbose:
         print("[build] " + " ".join(cmd), flush=True)
-    return lib, tmp, subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
-
-
-def _finish(job, verbose):
-    lib, tmp, proc = job
-    _, stderr = proc.communicate()
+    proc = subprocess.run(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
     noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in stderr.splitlines() if noise not in l)
+    err = "\n".join(l for l in proc.stderr.splitlines() if noise not in l)
     if proc.returncode != 0:
-        raise RuntimeError(f"compiler failed for {os.path.basename(lib)} ({proc.returncode}):\n{err}")
+        raise RuntimeError(f"compiler failed for {os.path.basename(cmd[-1])} ({proc.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
-    os.replace(tmp, lib)
-    return lib
-
-
-def _build_one(lib, sources, verbose, defines=()):
-    return _finish(_start(lib, sources, defines, verbose), verbose)
 
 
 def torch_command(out):
@@ -98,20 +91,22 @@ def torch_command(out):
 
 
 def build(verbose=True):
-    """Compiles the four libraries (two hipcc processes at a time), then the
-    marshalling module; returns the path of libqknorm.so."""
-    jobs = [(CEIL_LIB, CEIL_SOURCES, ()), (CEIL_CLOCKS_LIB, CEIL_SOURCES, ("QKNORM_BLOCK_CLOCKS",)),
-            (CLOCKS_LIB, SOURCES, ("QKNORM_BLOCK_CLOCKS",)), (LIB, SOURCES, ())]
-    for a, b in (jobs[:2], jobs[2:]):
-        running = [_start(lib, src, defs, verbose) for lib, src, defs in (a, b)]
-        for job in running:
-            _finish(job, verbose)
-    tmp = TORCH_LIB + ".tmp"
-    cmd = torch_command(tmp)
-    if verbose:
-        print("[build] " + " ".join(cmd), flush=True)
-    _finish((TORCH_LIB, tmp, subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                              text=True)), verbose)
+    """Compiles every source of the four libraries into an object of its own, links
+    them, then the marshalling module; returns the path of libqknorm.so."""
+    libs = [(LIB, SOURCES, ()), (CLOCKS_LIB, SOURCES, ("QKNORM_BLOCK_CLOCKS",)), (CEIL_LIB, CEIL_SOURCES, ()),
+            (CEIL_CLOCKS_LIB, CEIL_SOURCES, ("QKNORM_BLOCK_CLOCKS",))]
+    with tempfile.TemporaryDirectory() as tmp, concurrent.futures.ThreadPoolExecutor(JOBS) as pool:
+        objects = {lib: [os.path.join(tmp, f"{os.path.basename(lib)}.{s}.o") for s in sources]
+                   for lib, sources, _ in libs}
+        jobs = [pool.submit(_run, command(o, [s], defines), verbose)
+                for lib, sources, defines in libs for s, o in zip(sources, objects[lib])]
+        for job in jobs:
+            job.result()
+        for lib, _, _ in libs:
+            _run(command(lib + ".tmp", objects[lib], link=True), verbose)
+            os.replace(lib + ".tmp", lib)
+    _run(torch_command(TORCH_LIB + ".tmp"), verbose)
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     return LIB
 
 

@@ -46,33 +46,13 @@
 
 #include <string>
 
-#include "qknorm_device.hpp"
-#include "qknorm_internal.hpp"
-#include "qknorm_ops.hpp"
+#include "qknorm_attend_device.hpp"
 
 namespace qkn {
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
-
 constexpr int kWaves = 4;
 constexpr uint32_t kTopScale = 252;       // largest scale byte of a finite block; above it, NaN
-// A row's reference maximum follows its scores only when they pass it by 2^8:
-// float32 sums and bf16 probabilities keep their relative accuracy at any
-// scale, and the accumulator is hardly ever rescaled.
-constexpr float kSlack = 8.0f;
-// The reference before any score: the lowest finite value, so that every score
-// that is finite in base 2 (times log2 e) counts. Differences to it may be
-// infinite, never NaN.
-constexpr float kNothing = -3.40282347e38f;
-
-struct Frag {
-  uint32_t w[4];
-  __device__ __forceinline__ bf16x8_t get() const { return __builtin_bit_cast(bf16x8_t, *this); }
-};
-
 template <int SEL>
 __device__ __forceinline__ uint32_t widen_pair(uint32_t codes, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, SEL));
@@ -84,63 +64,6 @@ __device__ __forceinline__ uint32_t widen_byte(uint32_t codes, float scale, int 
     case 2: return widen_pair<2>(codes, scale);
     default: return widen_pair<3>(codes, scale);
   }
-}
-
-// The largest of three, NaN where one of them is: one v_maximum3_f32. (fmaxf
-// would spend an instruction per operand on quieting NaNs. Written as inline
-// asm it would read the scores without the wait states that a matrix product's
-// result needs, which the compiler puts only before instructions it knows.) A
-// row with a NaN score is NaN whatever its maximum.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
-}
-
-// In a branch that few tiles take: keeps the compiler from running it for all
-// of them as selects (the edge masks alone are 96 instructions of a tile).
-__device__ __forceinline__ void keep_branch() { asm volatile(""); }
-
-__device__ __forceinline__ float row_max(float v) {   // over the four lanes that hold a row
-  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[1]));
-  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return max3(__uint_as_float(p[0]), __uint_as_float(p[1]), __uint_as_float(p[1]));
-}
-
-// A sequence's query rows and cached length, held to what the arrays hold.
-struct Sequence {
-  int q0, nq, len;
-};
-__device__ __forceinline__ Sequence sequence(const AttendArgs& a, int b) {
-  Sequence s{b, 1, load_uniform(a.seq_lens + b)};
-  if (a.cu_q) {
-    const int q0 = load_uniform(a.cu_q + b), q1 = load_uniform(a.cu_q + b + 1);
-    s.q0 = q0 < 0 ? 0 : q0 > a.T ? a.T : q0;
-    s.nq = (q1 < s.q0 ? s.q0 : q1 > a.T ? a.T : q1) - s.q0;
-  }
-  s.len = s.len < 0 ? 0 : s.len > a.table_tokens ? a.table_tokens : s.len;
-  return s;
-}
-// Tokens [lo, hi) that query i of a sequence sees.
-__device__ __forceinline__ int see_hi(const AttendArgs& a, const Sequence& s, int i) {
-  const int pos = s.len - s.nq + i;
-  return pos < 0 ? 0 : a.causal ? pos + 1 : s.len;
-}
-__device__ __forceinline__ int see_lo(const AttendArgs& a, const Sequence& s, int i) {
-  const int lo = s.len - s.nq + i - a.window + 1;
-  return a.window && lo > 0 ? lo : 0;
-}
-// A block's rows r0 .. : what they see together, and the chunks that takes.
-struct Span {
-  int first, hi;     // first: a multiple of 32
-  int chunks;
-};
-__device__ __forceinline__ Span span(const AttendArgs& a, const Sequence& s, int i_first, int i_last) {
-  Span p;
-  const int lo = see_lo(a, s, i_first);
-  p.hi = see_hi(a, s, i_last);
-  p.first = lo & ~31;
-  p.chunks = p.hi > lo ? (int)((uint32_t)(p.hi - p.first + a.chunk - 1) / (uint32_t)a.chunk) : 0;
-  return p;
 }
 
 // Codes and scales of one 32-token tile, as one lane holds them: lane = 16 g
@@ -650,7 +573,7 @@ __global__ void __launch_bounds__(64 * kWaves, RT * D <= 128 ? 3 : 2) qknorm_att
 
 // Joins the chunks of rows whose cache was split: a block per (query, head),
 // D/4 threads across the row's columns, the rest along the chunks. The row's
-// chunk count follows from the same arithmetic as in qknorm_attend; rows
+// chunk count follows from the same arithmetic as in the attention kernels; rows
 // finished there are left alone. About 5 us as a launch of its own, mostly
 // start-up and two round trips to memory (86 parts of 40 rows, 1.8 MB).
 template <int D>
@@ -742,6 +665,21 @@ void (*pick_attend(int rt))(const AttendArgs) {
 
 }  // namespace
 
+int launch_attend_join(const AttendPlan& p, const AttendArgs& args, void* stream, std::string* err) {
+  AttendArgs a = args;
+  int rt = p.row_tile;
+  int mq = (int)p.max_q;
+  void* kargs[] = {&a, &rt, &mq};
+  const void* join = p.head_dim == 64    ? reinterpret_cast<const void*>(qknorm_attend_join<64>)
+                     : p.head_dim == 128 ? reinterpret_cast<const void*>(qknorm_attend_join<128>)
+                                         : reinterpret_cast<const void*>(qknorm_attend_join<256>);
+  const hipError_t e = hipLaunchKernel(join, dim3((unsigned)(a.B * mq), (unsigned)(a.heads_k * a.group)), dim3(256),
+                                       kargs, 0, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) return 0;
+  *err = std::string("kernel launch: ") + hipGetErrorString(e);
+  return (int)e;
+}
+
 int launch_attend(const AttendPlan& p, const AttendArgs& args, void* stream, std::string* err) {
   void (*fn)(const AttendArgs) = p.head_dim == 64    ? pick_attend<64>(p.row_tile)
                                  : p.head_dim == 128 ? pick_attend<128>(p.row_tile)
@@ -755,16 +693,7 @@ int launch_attend(const AttendPlan& p, const AttendArgs& args, void* stream, std
   const int64_t grid = (int64_t)a.B * a.heads_k * a.row_tiles * a.splits;
   hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)grid), dim3(64 * kWaves), kargs, 0,
                                  static_cast<hipStream_t>(stream));
-  if (e == hipSuccess && a.splits > 1) {
-    int rt = p.row_tile;
-    int mq = (int)p.max_q;
-    void* jargs[] = {&a, &rt, &mq};
-    const void* join = p.head_dim == 64    ? reinterpret_cast<const void*>(qknorm_attend_join<64>)
-                       : p.head_dim == 128 ? reinterpret_cast<const void*>(qknorm_attend_join<128>)
-                                           : reinterpret_cast<const void*>(qknorm_attend_join<256>);
-    e = hipLaunchKernel(join, dim3((unsigned)(a.B * mq), (unsigned)(a.heads_k * a.group)), dim3(256), jargs, 0,
-                        static_cast<hipStream_t>(stream));
-  }
+  if (e == hipSuccess && a.splits > 1) return launch_attend_join(p, a, stream, err);
   if (e != hipSuccess) {
     *err = std::string("kernel launch: ") + hipGetErrorString(e);
     return (int)e;

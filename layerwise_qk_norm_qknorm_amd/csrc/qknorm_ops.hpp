@@ -1,6 +1,7 @@
 // Internal interface between the C ABI layer of the operators around headwise
 // QK-Norm (qknorm_ops_api.cpp: validation and planning, no HIP calls) and
-// their kernels (qknorm_rope.hip, qknorm_attend.hip).
+// their kernels (qknorm_rope.hip, qknorm_rope_paired.hip, qknorm_attend.hip,
+// qknorm_attend_wide.hip, qknorm_gather.hip).
 #pragma once
 
 #include <stddef.h>
@@ -47,6 +48,16 @@ struct RopePlan {
   int apart = 0;        // 1 (MXFP4): a launch for Q and one for K and V
 };
 
+// Positions on several axes (time, height, width): the axis of every angle, two
+// bits each, and how far apart the axes' positions lie.
+constexpr int kMostAxes = 4;
+struct RopeAxes {
+  int n;               // 0: one position a token
+  int mixed;           // 1: the angles of a lane's piece lie on different axes
+  int64_t ld;
+  uint32_t of[kRopeMaxHead / 2 / 16];
+};
+
 struct RopeSide {  // one of Q, K, V
   const void* x;
   void* y;
@@ -74,6 +85,7 @@ struct RopeArgs {
   const float* cos_sin;
   int64_t ld_table, n_positions;
   const int64_t* positions;
+  RopeAxes axes;
   float inv_div, eps;
   // appending only
   const int64_t* slots;
@@ -89,7 +101,7 @@ struct RopeArgs {
 constexpr int kRopeMaxWaves = 8;   // of a block, paired layout
 constexpr int kRopeWaves = 4;      // of a block, one chunk per lane
 
-enum RopeMode : int { ROPE_FORWARD = 0, ROPE_APPEND_ROWS = 1, ROPE_APPEND_MXFP4 = 2 };
+enum RopeMode : int { ROPE_FORWARD = 0, ROPE_APPEND_ROWS = 1, ROPE_APPEND_MXFP4 = 2, ROPE_APPEND_MXFP8 = 3 };
 
 int launch_rope(int mode, int dtype, bool interleaved, const RopePlan& plan, const RopeArgs& args, void* stream,
                 std::string* err);
@@ -119,6 +131,7 @@ struct RopeGradArgs {
   const float* cos_sin;
   int64_t ld_table, n_positions;
   const int64_t* positions;
+  RopeAxes axes;
   float inv_div, eps;
   float* partial;      // [rows][head_dim], see rope_grad_rows
 };
@@ -126,8 +139,8 @@ struct RopeGradArgs {
 constexpr int kGradWaves = 4;   // waves of a gradient block, each with tokens of its own
 
 // The kernel of the paired layout for a plan (NULL: none).
-const void* rope_paired_kernel(int mode, int dtype, bool interleaved, const RopePlan& plan);
-const void* rope_paired_grad_kernel(int dtype, bool interleaved, const RopePlan& plan);
+const void* rope_paired_kernel(int mode, int dtype, bool interleaved, bool axes, const RopePlan& plan);
+const void* rope_paired_grad_kernel(int dtype, bool interleaved, bool axes, const RopePlan& plan);
 
 // Rows of partial gamma gradients a launch writes.
 int64_t rope_grad_rows(const RopeGradArgs& a);
@@ -143,6 +156,8 @@ struct AttendArgs {
   const uint8_t* cache[2];    // K, V codes
   const uint8_t* scales[2];
   int64_t page_stride, head_stride, scale_page_stride, scale_head_stride;   // bytes
+  int64_t token_stride;       // bytes
+  int scale_row;              // scale bytes of a token's head
   uint32_t n_pages;      // at most 2^31 - 1: ids are int32
   int log2_page;
   int heads_k, group;    // query heads per key head
@@ -174,5 +189,33 @@ struct AttendPlan {
 };
 
 int launch_attend(const AttendPlan& plan, const AttendArgs& args, void* stream, std::string* err);
+
+// Adds up the parts of rows whose cache was split.
+int launch_attend_join(const AttendPlan& plan, const AttendArgs& args, void* stream, std::string* err);
+
+// Caches of bf16 rows and MXFP8 (mx8). row_tile 1 and 2: the kernel whose waves
+// share a block's rows; 8 and 16: the one whose waves take 32 and 64 rows each.
+int launch_attend_wide(bool mx8, const AttendPlan& plan, const AttendArgs& args, void* stream, std::string* err);
+
+struct GatherArgs {
+  const char* cache[2];    // K, V; NULL out: not wanted
+  const uint8_t* scales[2];
+  char* out[2];
+  int64_t ld[2];           // bytes
+  int64_t page_stride, head_stride, token_stride, scale_page_stride, scale_head_stride;   // bytes
+  const int64_t* slots;
+  int64_t T, n_tokens_held;
+  int log2_page;
+  int head_dim;
+  int pieces;              // of a token's head
+  int items;               // pieces of a token's heads
+  int groups;              // waves of 64 items that a token's heads take
+  Divisor by_pieces, by_groups;
+  uint32_t units;          // waves of the launch
+  int64_t tokens;          // that these cover; the rest loop
+};
+enum GatherKind : int { GATHER_ROWS = 0, GATHER_MXFP4 = 1, GATHER_MXFP8 = 2 };
+// piece_bytes: of the rows written, 16 (MX formats: eight elements in 16-byte stores) or one element.
+int launch_gather(int kind, int dtype, int piece_bytes, const GatherArgs& args, void* stream, std::string* err);
 
 }  // namespace qkn

@@ -1,6 +1,6 @@
 // C ABI of the operators around headwise QK-Norm: argument validation and
-// planning for the norm with the rotation, its gradients, the paged append
-// and attention over the 4-bit cache. Plain C++ with no HIP call, as
+// planning for the norm with the rotation, its gradients, the paged append,
+// reading a cache back and attention over it. Plain C++ with no HIP call, as
 // qknorm_api.cpp; only the qkn::launch_* functions touch the HIP runtime.
 
 #include <algorithm>
@@ -70,6 +70,35 @@ int check_common(const char* fn, int64_t T, int dtype, bool fp8, float eps, int6
   }
   return QKNORM_OK;
 }
+
+// Positions on several axes, where there is a rotation.
+int check_axes(const char* fn, const qknorm_rope_t* rope, const qknorm_axes_t* axes, int64_t T) {
+  if (!axes || !rope || !rope->rot_dim) return QKNORM_OK;
+  if (axes->n_axes < 1 || axes->n_axes > QKNORM_MAX_AXES)
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: n_axes = %d is not in [1, %d]", fn, axes->n_axes, QKNORM_MAX_AXES);
+  if (!axes->axis) return fail(QKNORM_ERR_INVALID_ARG, "%s: axes->axis is required", fn);
+  for (int64_t i = 0; i < rope->rot_dim / 2; ++i)
+    if (axes->axis[i] >= axes->n_axes)
+      return fail(QKNORM_ERR_INVALID_ARG, "%s: axis %d of angle %lld is not below n_axes = %d", fn, axes->axis[i],
+                  (long long)i, axes->n_axes);
+  if (axes->ld_positions < 0 || !fits(axes->n_axes, axes->ld_positions, T, 8))
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: ld_positions = %lld", fn, (long long)axes->ld_positions);
+  return QKNORM_OK;
+}
+
+// What the kernels take of them. `angles` of a lane's piece go together where they
+// share an axis.
+void axes_args(const qknorm_rope_t* rope, const qknorm_axes_t* axes, int angles, RopeAxes* out) {
+  if (!axes || !rope || !rope->rot_dim || axes->n_axes == 1) return;   // n == 0: one axis
+  out->n = axes->n_axes;
+  out->ld = axes->ld_positions;
+  for (int64_t i = 0; i < rope->rot_dim / 2; ++i) {
+    out->of[i >> 4] |= (uint32_t)axes->axis[i] << (2 * (i & 15));
+    if (axes->axis[i] != axes->axis[i - i % angles]) out->mixed = 1;
+  }
+}
+// Angles of a lane's piece: of a whole chunk, or of a pair of pieces.
+int angles_of(const RopePlan& p, bool inter) { return p.whole && inter ? p.vw / 2 : p.vw; }
 
 int check_width(const char* fn, const char* nm, int64_t h, int64_t head_dim) {
   if (h <= 0 || h % head_dim)
@@ -172,9 +201,9 @@ Region table_region(const qknorm_rope_t* rope) {
   if (!rope || !rope->rot_dim) return Region{0, 1, 0, 0, 1};
   return Region{(uintptr_t)rope->cos_sin, rope->ld, rope->rot_dim, rope->n_positions, 4};
 }
-Region positions_region(const qknorm_rope_t* rope, int64_t T) {
+Region positions_region(const qknorm_rope_t* rope, const qknorm_axes_t* axes, int64_t T) {
   if (!rope || !rope->rot_dim) return Region{0, 1, 0, 0, 1};
-  return bytes_of(rope->positions, T * 8);
+  return bytes_of(rope->positions, ((axes ? (axes->n_axes - 1) * axes->ld_positions : 0) + T) * 8);
 }
 Region gamma_region(const void* gamma, int64_t h, int64_t head_dim, int64_t gstride, int dtype) {
   return bytes_of(gamma, gamma ? ((h / head_dim - 1) * gstride + head_dim) * (int64_t)gamma_size(dtype) : 0);
@@ -186,45 +215,56 @@ struct RopeChecked {
   RopeArgs args;
 };
 
+bool coded(const qknorm_cache_t* c) { return c->format != QKNORM_CACHE_ROWS; }
+const char* format_name(const qknorm_cache_t* c) { return c->format == QKNORM_CACHE_MXFP4 ? "MXFP4" : "MXFP8"; }
+// Elements of the row type, or bytes of codes, of a token's head.
+int64_t held_row(const qknorm_cache_t* c, int64_t head_dim) {
+  return c->format == QKNORM_CACHE_MXFP4 ? head_dim / 2 : head_dim;
+}
+
 int check_cache(const char* fn, const qknorm_cache_t* c, int64_t head_dim, int64_t esz, bool need_pointers) {
   if (!c) return fail(QKNORM_ERR_INVALID_ARG, "%s: a cache descriptor is required", fn);
-  if (c->format != QKNORM_CACHE_ROWS && c->format != QKNORM_CACHE_MXFP4)
+  if (c->format != QKNORM_CACHE_ROWS && c->format != QKNORM_CACHE_MXFP4 && c->format != QKNORM_CACHE_MXFP8)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: unknown cache format %d", fn, c->format);
-  const bool four = c->format == QKNORM_CACHE_MXFP4;
+  const bool codes = coded(c);
   if (c->heads <= 0 || c->heads > kMaxWidth / head_dim)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: cache->heads = %lld", fn, (long long)c->heads);
   if (c->n_pages <= 0 || !power_of_two(c->page_size) || c->page_size > ((int64_t)1 << 30))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the cache needs pages, and a power of two of tokens in each", fn);
-  if (four && head_dim % 32)
-    return fail(QKNORM_ERR_INVALID_ARG, "%s: head_dim = %lld is not a multiple of 32 (MXFP4)", fn,
-                (long long)head_dim);
-  if (four && c->page_size < 16) return fail(QKNORM_ERR_INVALID_ARG, "%s: MXFP4 pages hold at least 16 tokens", fn);
-  const int64_t row = four ? head_dim / 2 : head_dim;   // a token's elements or bytes in one head
+  if (codes && head_dim % 32)
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: head_dim = %lld is not a multiple of 32 (%s)", fn, (long long)head_dim,
+                format_name(c));
+  if (codes && c->page_size < 16)
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: %s pages hold at least 16 tokens", fn, format_name(c));
+  const int64_t row = held_row(c, head_dim);
   if (c->token_stride < row || c->head_stride < row || c->page_stride < row)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: cache strides must hold a token's head", fn);
   // positions of all tokens in a page and head, of all heads, of all pages: byte ranges that fit
-  const int64_t unit = four ? 1 : esz;
+  const int64_t unit = codes ? 1 : esz;
   const int64_t lim = INT64_MAX / 4 / unit;
   if (c->token_stride > lim / c->page_size || c->head_stride > lim / c->heads || c->page_stride > lim / c->n_pages)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the cache exceeds the address range", fn);
   if (c->n_pages > lim / c->page_size)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the cache has too many tokens", fn);
-  if (four) {
-    if (c->token_stride != head_dim / 2)
+  if (codes) {
+    if (c->format == QKNORM_CACHE_MXFP4 && c->token_stride != head_dim / 2)
       return fail(QKNORM_ERR_INVALID_ARG, "%s: MXFP4 tokens of a head are packed (token_stride = head_dim / 2)", fn);
     const int64_t srow = head_dim / 32;
     if (c->scale_page_stride < srow || c->scale_head_stride < srow || c->scale_page_stride > lim / c->n_pages ||
         c->scale_head_stride > lim / c->heads)
       return fail(QKNORM_ERR_INVALID_ARG, "%s: scale strides must hold a token's scales", fn);
     if (c->page_stride % 16 || c->head_stride % 16 || c->scale_page_stride % 16 || c->scale_head_stride % 16)
-      return fail(QKNORM_ERR_INVALID_ARG, "%s: MXFP4 page and head strides must be multiples of 16 bytes", fn);
+      return fail(QKNORM_ERR_INVALID_ARG, "%s: %s page and head strides must be multiples of 16 bytes", fn,
+                  format_name(c));
+    if (c->token_stride % 16)
+      return fail(QKNORM_ERR_INVALID_ARG, "%s: %s token strides must be multiples of 16 bytes", fn, format_name(c));
   }
   if (!need_pointers) return QKNORM_OK;
-  if (!c->k || !c->v || (four && (!c->k_scales || !c->v_scales)))
+  if (!c->k || !c->v || (codes && (!c->k_scales || !c->v_scales)))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: cache pointers are required", fn);
-  if (four && !(multiple(c->k, 16) && multiple(c->v, 16) && multiple(c->k_scales, 16) && multiple(c->v_scales, 16)))
-    return fail(QKNORM_ERR_INVALID_ARG, "%s: MXFP4 cache pointers must be 16-byte aligned", fn);
-  if (!four && !(multiple(c->k, esz) && multiple(c->v, esz)))
+  if (codes && !(multiple(c->k, 16) && multiple(c->v, 16) && multiple(c->k_scales, 16) && multiple(c->v_scales, 16)))
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: %s cache pointers must be 16-byte aligned", fn, format_name(c));
+  if (!codes && !(multiple(c->k, esz) && multiple(c->v, esz)))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: cache pointers must be aligned to their element size", fn);
   return QKNORM_OK;
 }
@@ -233,8 +273,7 @@ int check_cache(const char* fn, const qknorm_cache_t* c, int64_t head_dim, int64
 // outermost axis (so that arrays which take turns within one allocation's pages
 // are told apart), the whole span otherwise.
 Region cache_region(const qknorm_cache_t* c, const void* p, bool scales, int64_t head_dim, int64_t esz) {
-  const bool four = c->format == QKNORM_CACHE_MXFP4;
-  const int64_t unit = four ? 1 : esz, row = four ? head_dim / 2 : head_dim;
+  const int64_t unit = coded(c) ? 1 : esz, row = held_row(c, head_dim);
   const int64_t inner =
       scales ? (c->heads - 1) * c->scale_head_stride + c->page_size * (head_dim / 32)
              : ((c->heads - 1) * c->head_stride + (c->page_size - 1) * c->token_stride + row) * unit;
@@ -247,7 +286,6 @@ Region cache_region(const qknorm_cache_t* c, const void* p, bool scales, int64_t
 // and pages, apart: any nesting order of (page, head, token) with every stride
 // at least as large as what lies inside it.
 bool cache_nests(const qknorm_cache_t* c, int64_t head_dim) {
-  const bool four = c->format == QKNORM_CACHE_MXFP4;
   struct Axis {
     int64_t stride, n;
   };
@@ -255,13 +293,13 @@ bool cache_nests(const qknorm_cache_t* c, int64_t head_dim) {
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2 - i; ++j)
       if (ax[j].stride > ax[j + 1].stride) std::swap(ax[j], ax[j + 1]);
-  int64_t inner = four ? head_dim / 2 : head_dim;
+  int64_t inner = held_row(c, head_dim);
   for (const Axis& x : ax) {
     if (x.n == 1) continue;
     if (x.stride < inner) return false;
     inner = x.stride * (x.n - 1) + inner;
   }
-  if (!four) return true;
+  if (!coded(c)) return true;
   const int64_t page = c->page_size * (head_dim / 32);
   const int64_t lo = c->scale_head_stride < c->scale_page_stride ? c->scale_head_stride : c->scale_page_stride;
   const bool head_inner = c->scale_head_stride <= c->scale_page_stride;
@@ -274,12 +312,13 @@ bool cache_nests(const qknorm_cache_t* c, int64_t head_dim) {
 // Forward (v, cache and slots NULL) and append.
 int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v,
                int64_t T, int dtype, float eps, int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope,
-               const qknorm_cache_t* cache, const int64_t* slots, bool append, RopeChecked* out, bool* noop) {
+               const qknorm_axes_t* axes, const qknorm_cache_t* cache, const int64_t* slots, bool append,
+               RopeChecked* out, bool* noop) {
   *noop = false;
   if (!k || (!append && !q) || (append && !v))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: operand descriptors are required", fn);
   int rc = check_common(fn, T, dtype, !append, eps, head_dim, gstride, rope);
-  if (rc) return rc;
+  if (rc || (rc = check_axes(fn, rope, axes, T))) return rc;
   const int64_t esz = (int64_t)elem_size(dtype), gsz = (int64_t)gamma_size(dtype);
   const qknorm_operand_t* ops[3] = {q, k, v};
   const char* nm[3] = {"q", "k", "v"};
@@ -296,7 +335,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
     if (c < 2 && o->gamma && !multiple(o->gamma, gsz))
       return fail(QKNORM_ERR_INVALID_ARG, "%s: %s->gamma must be aligned to its element size", fn, nm[c]);
   }
-  const bool four = append && cache && cache->format == QKNORM_CACHE_MXFP4;
+  const bool codes = append && cache && coded(cache);
   if (append) {
     if ((rc = check_cache(fn, cache, head_dim, esz, T > 0))) return rc;
     if (k->h != cache->heads * head_dim || v->h != k->h)
@@ -326,12 +365,12 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
     if (c < 2 && o->gamma) ins[n_in++] = {gamma_region(o->gamma, o->h, head_dim, gstride, dtype), "gamma"};
   }
   ins[n_in++] = {table_region(rope), "the rope table"};
-  ins[n_in++] = {positions_region(rope, T), "positions"};
+  ins[n_in++] = {positions_region(rope, axes, T), "positions"};
   if (append) {
     ins[n_in++] = {bytes_of(slots, T * 8), "slots"};
     outs[n_out++] = {cache_region(cache, cache->k, false, head_dim, esz), "the k cache"};
     outs[n_out++] = {cache_region(cache, cache->v, false, head_dim, esz), "the v cache"};
-    if (four) {
+    if (codes) {
       outs[n_out++] = {cache_region(cache, cache->k_scales, true, head_dim, esz), "the k scales"};
       outs[n_out++] = {cache_region(cache, cache->v_scales, true, head_dim, esz), "the v scales"};
     }
@@ -357,7 +396,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
       if (!o) continue;
       al.need(o->x, pb);
       al.need(o->ld_x * esz, pb);
-      if (o->y && !(four && o != q && pb < 16)) {
+      if (o->y && !(codes && o != q && pb < 16)) {
         al.need(o->y, pb);
         al.need(o->ld_y * esz, pb);
       }
@@ -367,7 +406,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
         al.need(gstride * gsz, g);
       }
     }
-    if (append && !four) {
+    if (append && !codes) {
       al.need(cache->k, pb);
       al.need(cache->v, pb);
       al.need(cache->page_stride * esz, pb);
@@ -389,7 +428,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
   plan_waves(&p, slots_in, T);
   if (!p.whole && slots_in[0] + slots_in[1] + slots_in[2] > 65535)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: too many heads", fn);
-  p.apart = four && q && p.whole && p.slots > 1;
+  p.apart = codes && q && p.whole && p.slots > 1;
   a.n_slots = slots_in[0] + slots_in[1] + slots_in[2];
   const int unit = p.whole ? p.slots : 1;   // sides begin at whole waves, or at slots
   a.first[1] = (slots_in[0] + unit - 1) / unit;
@@ -399,6 +438,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
   a.head_dim = (int)head_dim;
   a.pairs = p.pairs;
   table_args(rope, p, &a.rot, &a.rot_pairs, &a.cos_sin, &a.ld_table, &a.n_positions, &a.positions);
+  axes_args(rope, axes, angles_of(p, inter), &a.axes);
   a.log2_lanes = log2_of(p.lanes);
   a.half_lanes = rot && !inter ? (int)(rot / 2 / p.vw) : 0;
   a.idle = p.lanes * p.np * 2 * p.vw != head_dim;
@@ -408,7 +448,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
   a.inv_div = (float)(1.0 / (double)head_dim);
   a.eps = eps;
   if (append) {
-    const int64_t unit = four ? 1 : esz;
+    const int64_t unit = codes ? 1 : esz;
     a.slots = slots;
     a.n_tokens_held = cache->n_pages * cache->page_size;
     a.log2_page = log2_of(cache->page_size);
@@ -463,14 +503,13 @@ size_t grad_workspace(int64_t heads_q, int64_t heads_k, int64_t T, int dtype, in
   return most;
 }
 
-int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T, int dtype, float eps,
-               int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope, void* ws, size_t ws_bytes,
-               RopePlan* plan, RopeGradArgs* args, bool* noop) {
-  const char* fn = "qknorm_headwise_rope_backward";
+int check_grad(const char* fn, const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T, int dtype,
+               float eps, int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope, const qknorm_axes_t* axes,
+               void* ws, size_t ws_bytes, RopePlan* plan, RopeGradArgs* args, bool* noop) {
   *noop = false;
   if (!q || !k) return fail(QKNORM_ERR_INVALID_ARG, "%s: q and k operand descriptors are required", fn);
   int rc = check_common(fn, T, dtype, false, eps, head_dim, gstride, rope);
-  if (rc) return rc;
+  if (rc || (rc = check_axes(fn, rope, axes, T))) return rc;
   if (gstride && gstride < head_dim)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: gamma_head_stride = %lld is neither 0 nor >= head_dim", fn,
                 (long long)gstride);
@@ -509,7 +548,7 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
     ins[n_in++] = gamma_region(o->gamma, o->h, head_dim, gstride, dtype);
   }
   ins[n_in++] = table_region(rope);
-  ins[n_in++] = positions_region(rope, T);
+  ins[n_in++] = positions_region(rope, axes, T);
   for (int c = 0; c < 2; ++c)
     if (ops[c]->dgamma) outs[n_out++] = gamma_region(ops[c]->dgamma, ops[c]->h, head_dim, gstride, QKNORM_F32);
   if (wanted) outs[n_out++] = bytes_of(ws, (int64_t)need);
@@ -556,6 +595,7 @@ int check_grad(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, i
   a.head_dim = (int)head_dim;
   a.pairs = plan->pairs;
   table_args(rope, *plan, &a.rot, &a.rot_pairs, &a.cos_sin, &a.ld_table, &a.n_positions, &a.positions);
+  axes_args(rope, axes, angles_of(*plan, rot && rope->interleaved), &a.axes);
   a.log2_lanes = log2_of(plan->lanes);
   a.half_lanes = rot && !rope->interleaved ? (int)(rot / 2 / plan->vw) : 0;
   a.idle = plan->lanes * plan->np * 2 * plan->vw != head_dim;
@@ -630,6 +670,37 @@ AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t
   return p;
 }
 
+// The same for caches of rows and MXFP8: up to 32 rows of a sequence share a block's
+// waves, beyond them each wave takes 32 rows of its own, and 64 from 129 rows on
+// (at 256 columns a wave's accumulators hold 32).
+AttendPlan plan_attend_wide(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t T, int64_t max_q,
+                            int64_t max_len, int64_t window) {
+  AttendPlan p;
+  p.head_dim = (int)head_dim;
+  const int64_t rows = max_q * group;
+  p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 128 || head_dim == 256 ? 8 : 16;
+  const int64_t tiles = (rows + 16 * p.row_tile - 1) / (16 * p.row_tile);
+  const int64_t resident = 256 * (head_dim == 256 || (p.row_tile == 16 && head_dim == 128) ? 1 : 2);
+  p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);
+  p.max_q = max_q;
+  const int64_t blocks = B * heads_k * p.row_tiles;
+  const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
+  p.most_splits = (int)most(max_len);
+  // what a block's rows see together, at most
+  const int64_t span = window && window < max_len ? std::min(max_len, window + 16 * p.row_tile / group + 33) : max_len;
+  const int64_t m = most(span);
+  int64_t least = INT64_MAX;
+  for (int64_t rounds = 0; rounds <= kRounds; ++rounds) {
+    const int64_t s = std::clamp<int64_t>(rounds * resident / blocks, 1, m);
+    int64_t chunk = ((span + s - 1) / s + 127) / 128 * 128;
+    if (chunk < 256) chunk = 256;
+    const int64_t n = (span + chunk - 1) / chunk;
+    const int64_t cost = (blocks * n + resident - 1) / resident * (chunk / 128 + kBlockSteps) + (n > 1 ? kJoinSteps : 0);
+    if (cost < least) least = cost, p.splits = (int)n, p.chunk = (int)chunk;
+  }
+  return p;
+}
+
 bool attend_sizes_ok(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B, int64_t max_q,
                      int64_t max_len) {
   return T >= 0 && heads_k > 0 && heads_q > 0 && heads_q % heads_k == 0 && heads_q <= 65536 &&
@@ -642,17 +713,13 @@ size_t attend_workspace(const AttendPlan& p, int64_t T, int64_t heads_q) {
   return (size_t)T * (size_t)heads_q * (size_t)p.most_splits * (size_t)(p.head_dim + 2) * 4;
 }
 
-}  // namespace
-
-extern "C" {
-
-int qknorm_headwise_rope(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype, float eps,
-                         int64_t head_dim, int64_t gamma_head_stride, const qknorm_rope_t* rope, void* stream) {
-  const char* fn = "qknorm_headwise_rope";
+int rope_forward(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype, float eps,
+                 int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope, const qknorm_axes_t* axes,
+                 void* stream) {
   RopeChecked c;
   bool noop;
-  const int rc = check_rope(fn, q, k, nullptr, T, dtype, eps, head_dim, gamma_head_stride, rope, nullptr, nullptr,
-                            false, &c, &noop);
+  const int rc = check_rope(fn, q, k, nullptr, T, dtype, eps, head_dim, gstride, rope, axes, nullptr, nullptr, false,
+                            &c, &noop);
   if (rc || noop) return rc;
   std::string err;
   if (launch_rope(ROPE_FORWARD, dtype, c.args.rot && rope->interleaved, c.plan, c.args, stream, &err))
@@ -660,49 +727,122 @@ int qknorm_headwise_rope(const qknorm_operand_t* q, const qknorm_operand_t* k, i
   return ok();
 }
 
-int qknorm_headwise_rope_backward(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T,
-                                  int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
-                                  const qknorm_rope_t* rope, void* workspace, size_t workspace_bytes, void* stream) {
+int rope_backward(const char* fn, const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T, int dtype,
+                  float eps, int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope, const qknorm_axes_t* axes,
+                  void* workspace, size_t workspace_bytes, void* stream) {
   RopePlan plan;
   RopeGradArgs args;
   bool noop;
-  const int rc = check_grad(q, k, T, dtype, eps, head_dim, gamma_head_stride, rope, workspace, workspace_bytes, &plan,
+  const int rc = check_grad(fn, q, k, T, dtype, eps, head_dim, gstride, rope, axes, workspace, workspace_bytes, &plan,
                             &args, &noop);
   if (rc || noop) return rc;
   std::string err;
   if (launch_rope_grad(dtype, args.rot && rope->interleaved, plan, args, stream, &err))
-    return fail(QKNORM_ERR_HIP, "qknorm_headwise_rope_backward: %s", err.c_str());
+    return fail(QKNORM_ERR_HIP, "%s: %s", fn, err.c_str());
   return ok();
 }
 
-size_t qknorm_headwise_rope_backward_workspace(int64_t hq, int64_t hk, int64_t T, int dtype, int64_t head_dim,
-                                               int64_t gamma_head_stride) {
-  if (T <= 0 || head_dim <= 0 || head_dim > kRopeMaxHead || hq <= 0 || hk <= 0 || hq % head_dim || hk % head_dim ||
-      hq > kMaxWidth || hk > kMaxWidth || (dtype != QKNORM_F32 && dtype != QKNORM_BF16) || gamma_head_stride < 0)
-    return 0;
-  return grad_workspace(hq / head_dim, hk / head_dim, T, dtype, head_dim, gamma_head_stride);
-}
-
-int qknorm_paged_append(const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
-                        int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride, const qknorm_rope_t* rope,
-                        const qknorm_cache_t* cache, const int64_t* slots, void* stream) {
-  const char* fn = "qknorm_paged_append";
+int append(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
+           int dtype, float eps, int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope,
+           const qknorm_axes_t* axes, const qknorm_cache_t* cache, const int64_t* slots, void* stream) {
   RopeChecked c;
   bool noop;
-  const int rc = check_rope(fn, q, k, v, T, dtype, eps, head_dim, gamma_head_stride, rope, cache, slots, true, &c,
-                            &noop);
+  const int rc = check_rope(fn, q, k, v, T, dtype, eps, head_dim, gstride, rope, axes, cache, slots, true, &c, &noop);
   if (rc || noop) return rc;
   std::string err;
-  const int mode = cache->format == QKNORM_CACHE_MXFP4 ? ROPE_APPEND_MXFP4 : ROPE_APPEND_ROWS;
+  const int mode = cache->format == QKNORM_CACHE_MXFP4   ? ROPE_APPEND_MXFP4
+                   : cache->format == QKNORM_CACHE_MXFP8 ? ROPE_APPEND_MXFP8
+                                                         : ROPE_APPEND_ROWS;
   if (launch_rope(mode, dtype, c.args.rot && rope->interleaved, c.plan, c.args, stream, &err))
     return fail(QKNORM_ERR_HIP, "%s: %s", fn, err.c_str());
   return ok();
 }
 
-int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const qknorm_cache_t* cache,
-                        int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window,
-                        void* workspace, size_t workspace_bytes, void* stream) {
-  const char* fn = "qknorm_paged_attend";
+// -------------------------------------------------------------------- gather
+int gather(const char* fn, const qknorm_cache_t* cache, int64_t head_dim, const int64_t* slots, int64_t T, int dtype,
+           void* k_rows, int64_t ld_k, void* v_rows, int64_t ld_v, void* stream) {
+  if (!elem_size(dtype)) return fail(QKNORM_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (dtype == QKNORM_FP8_E4M3)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: FP8 rows are not supported (float32 or bf16)", fn);
+  if (T < 0) return fail(QKNORM_ERR_INVALID_ARG, "%s: T = %lld < 0", fn, (long long)T);
+  if (head_dim <= 0) return fail(QKNORM_ERR_INVALID_ARG, "%s: head_dim = %lld", fn, (long long)head_dim);
+  if (head_dim > kRopeMaxHead)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: head_dim = %lld > %d", fn, (long long)head_dim, kRopeMaxHead);
+  const int64_t esz = (int64_t)elem_size(dtype);
+  int rc = check_cache(fn, cache, head_dim, esz, T > 0);
+  if (rc) return rc;
+  const int64_t h = cache->heads * head_dim;
+  if (T > 0 && !k_rows && !v_rows) return fail(QKNORM_ERR_INVALID_ARG, "%s: k_rows or v_rows is required", fn);
+  if (k_rows && (rc = check_rows(fn, "k_rows", k_rows, ld_k, h, T, esz))) return rc;
+  if (v_rows && (rc = check_rows(fn, "v_rows", v_rows, ld_v, h, T, esz))) return rc;
+  if (T > 0 && (!slots || !multiple(slots, 8)))
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: slots must be an 8-byte aligned device pointer", fn);
+  if (T == 0) return ok();
+  const bool codes = coded(cache);
+  const Region outs[] = {Region{(uintptr_t)k_rows, ld_k, h, k_rows ? T : 0, esz},
+                         Region{(uintptr_t)v_rows, ld_v, h, v_rows ? T : 0, esz}};
+  const Region ins[] = {cache_region(cache, cache->k, false, head_dim, esz),
+                        cache_region(cache, cache->v, false, head_dim, esz),
+                        codes ? cache_region(cache, cache->k_scales, true, head_dim, esz) : Region{},
+                        codes ? cache_region(cache, cache->v_scales, true, head_dim, esz) : Region{},
+                        bytes_of(slots, T * 8)};
+  if (may_overlap(outs[0], outs[1])) return fail(QKNORM_ERR_INVALID_ARG, "%s: k_rows overlaps v_rows", fn);
+  for (const Region& out : outs)
+    for (const Region& in : ins)
+      if (may_overlap(out, in)) return fail(QKNORM_ERR_INVALID_ARG, "%s: the rows overlap the cache or slots", fn);
+
+  const int64_t unit = codes ? 1 : esz;
+  Aligned al;
+  for (const Region& r : outs)
+    if (r.T) {
+      al.need((const void*)r.base, 16);
+      al.need(r.ld * esz, 16);
+    }
+  if (!codes) {
+    al.need(cache->k, 16);
+    al.need(cache->v, 16);
+    al.need(cache->page_stride * esz, 16);
+    al.need(cache->head_stride * esz, 16);
+    al.need(cache->token_stride * esz, 16);
+    al.need(head_dim * esz, 16);
+  }
+  const int piece_bytes = al.ok ? 16 : (int)esz;
+  GatherArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.cache[0] = (const char*)cache->k;
+  a.cache[1] = (const char*)cache->v;
+  a.scales[0] = (const uint8_t*)cache->k_scales;
+  a.scales[1] = (const uint8_t*)cache->v_scales;
+  a.out[0] = (char*)k_rows;
+  a.out[1] = (char*)v_rows;
+  a.ld[0] = ld_k * esz;
+  a.ld[1] = ld_v * esz;
+  a.page_stride = cache->page_stride * unit;
+  a.head_stride = cache->head_stride * unit;
+  a.token_stride = cache->token_stride * unit;
+  a.scale_page_stride = cache->scale_page_stride;
+  a.scale_head_stride = cache->scale_head_stride;
+  a.slots = slots;
+  a.T = T;
+  a.n_tokens_held = cache->n_pages * cache->page_size;
+  a.log2_page = log2_of(cache->page_size);
+  a.head_dim = (int)head_dim;
+  a.pieces = (int)(codes ? head_dim / 8 : head_dim * esz / piece_bytes);
+  a.items = (int)(cache->heads * a.pieces);
+  a.groups = (a.items + 63) / 64 * (k_rows && v_rows ? 2 : 1);
+  const int kind = cache->format == QKNORM_CACHE_ROWS    ? GATHER_ROWS
+                   : cache->format == QKNORM_CACHE_MXFP4 ? GATHER_MXFP4
+                                                         : GATHER_MXFP8;
+  std::string err;
+  if (launch_gather(kind, dtype, piece_bytes, a, stream, &err))
+    return fail(QKNORM_ERR_HIP, "%s: %s", fn, err.c_str());
+  return ok();
+}
+
+// Attention over MXFP4, or (wide) over rows and MXFP8.
+int attend(const char* fn, bool wide, const qknorm_operand_t* q, int64_t T, int dtype, const qknorm_cache_t* cache,
+           int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window, void* workspace,
+           size_t workspace_bytes, void* stream) {
   if (!q || !cache || !batch) return fail(QKNORM_ERR_INVALID_ARG, "%s: q, cache and batch are required", fn);
   if (!elem_size(dtype)) return fail(QKNORM_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
   if (dtype != QKNORM_BF16) return fail(QKNORM_ERR_UNSUPPORTED, "%s: query rows are bf16", fn);
@@ -710,13 +850,17 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   if (head_dim != 64 && head_dim != 128 && head_dim != 256)
     return fail(head_dim > 0 ? QKNORM_ERR_UNSUPPORTED : QKNORM_ERR_INVALID_ARG, "%s: head_dim = %lld (64, 128 or 256)",
                 fn, (long long)head_dim);
-  if (cache->format == QKNORM_CACHE_ROWS)
+  if (!wide && (cache->format == QKNORM_CACHE_ROWS || cache->format == QKNORM_CACHE_MXFP8))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the cache must be MXFP4", fn);
+  if (wide && cache->format == QKNORM_CACHE_MXFP4)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: the cache must be rows or MXFP8", fn);
   if (!(std::isfinite(scale) && scale > 0.0f))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
   if (window < 0) return fail(QKNORM_ERR_INVALID_ARG, "%s: window = %lld < 0", fn, (long long)window);
   const bool none = T == 0 || batch->B == 0;
-  int rc = check_cache(fn, cache, head_dim, 1, !none);
+  const bool codes = cache->format != QKNORM_CACHE_ROWS;
+  const int64_t unit = codes ? 1 : 2;      // bytes of the strides' elements
+  int rc = check_cache(fn, cache, head_dim, unit, !none);
   if (rc) return rc;
   if ((rc = check_width(fn, "q", q->h, head_dim))) return rc;
   const int64_t heads_q = q->h / head_dim;
@@ -740,6 +884,14 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   if (none) return ok();
   if (!multiple(q->x, 16) || !multiple(q->y, 16) || (T > 1 && (q->ld_x % 8 || q->ld_y % 8)))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: query and output rows must be 16-byte aligned", fn);
+  if (wide && cache->page_size < 16)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: pages of fewer than 16 tokens", fn);
+  if (!codes && !(multiple(cache->k, 16) && multiple(cache->v, 16) && cache->page_stride % 8 == 0 &&
+                  cache->head_stride % 8 == 0 && cache->token_stride % 8 == 0))
+    return fail(QKNORM_ERR_INVALID_ARG, "%s: cache pointers and strides must be multiples of 16 bytes", fn);
+  // a lane's offset among the tokens that one load takes is 32 bits
+  if (cache->token_stride > (((int64_t)1 << 32) - 1024) / 16 / unit)
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: cache->token_stride = %lld", fn, (long long)cache->token_stride);
   if (!batch->block_table || !batch->seq_lens)
     return fail(QKNORM_ERR_INVALID_ARG, "%s: block_table and seq_lens are required", fn);
   if (!multiple(batch->block_table, 4) || !multiple(batch->seq_lens, 4) || !multiple(batch->cu_q, 4))
@@ -750,7 +902,8 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   const int64_t max_len = batch->max_len < capacity ? batch->max_len : capacity;
   if (!attend_sizes_ok(T, heads_q, cache->heads, head_dim, batch->B, max_q, max_len))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
-  AttendPlan p = plan_attend(head_dim, cache->heads, heads_q / cache->heads, batch->B, T, max_q, max_len, window);
+  AttendPlan p = (wide ? plan_attend_wide : plan_attend)(head_dim, cache->heads, heads_q / cache->heads, batch->B, T,
+                                                         max_q, max_len, window);
   if ((int64_t)batch->B * cache->heads * p.row_tiles > kLaunchThreads / 256 / p.splits)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the launch exceeds the grid", fn);
   const size_t need = attend_workspace(p, T, heads_q);
@@ -763,10 +916,10 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   const Region y{(uintptr_t)q->y, q->ld_y, q->h, T, 2};
   const Region ws = bytes_of(workspace, (int64_t)need);
   const Region ins[] = {Region{(uintptr_t)q->x, q->ld_x, q->h, T, 2},
-                        cache_region(cache, cache->k, false, head_dim, 1),
-                        cache_region(cache, cache->v, false, head_dim, 1),
-                        cache_region(cache, cache->k_scales, true, head_dim, 1),
-                        cache_region(cache, cache->v_scales, true, head_dim, 1),
+                        cache_region(cache, cache->k, false, head_dim, unit),
+                        cache_region(cache, cache->v, false, head_dim, unit),
+                        codes ? cache_region(cache, cache->k_scales, true, head_dim, 1) : Region{},
+                        codes ? cache_region(cache, cache->v_scales, true, head_dim, 1) : Region{},
                         bytes_of(batch->block_table, ((batch->B - 1) * batch->ld_table + batch->table_pages) * 4),
                         bytes_of(batch->seq_lens, batch->B * 4),
                         bytes_of(batch->cu_q, batch->cu_q ? (batch->B + 1) * 4 : 0)};
@@ -784,12 +937,16 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   a.T = (int)T;
   a.cache[0] = (const uint8_t*)cache->k;
   a.cache[1] = (const uint8_t*)cache->v;
-  a.scales[0] = (const uint8_t*)cache->k_scales;
-  a.scales[1] = (const uint8_t*)cache->v_scales;
-  a.page_stride = cache->page_stride;
-  a.head_stride = cache->head_stride;
-  a.scale_page_stride = cache->scale_page_stride;
-  a.scale_head_stride = cache->scale_head_stride;
+  a.page_stride = cache->page_stride * unit;
+  a.head_stride = cache->head_stride * unit;
+  a.token_stride = cache->token_stride * unit;
+  if (codes) {
+    a.scales[0] = (const uint8_t*)cache->k_scales;
+    a.scales[1] = (const uint8_t*)cache->v_scales;
+    a.scale_page_stride = cache->scale_page_stride;
+    a.scale_head_stride = cache->scale_head_stride;
+    a.scale_row = (int)(head_dim / 32);
+  }
   a.n_pages = (uint32_t)(cache->n_pages < INT32_MAX ? cache->n_pages : INT32_MAX);
   a.log2_page = log2_of(cache->page_size);
   a.heads_k = (int)cache->heads;
@@ -813,8 +970,81 @@ int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const q
   a.part_o = (float*)workspace;
   a.part_ml = need ? (float*)workspace + (size_t)T * heads_q * p.splits * p.head_dim : nullptr;
   std::string err;
-  if (launch_attend(p, a, stream, &err)) return fail(QKNORM_ERR_HIP, "%s: %s", fn, err.c_str());
+  if (wide ? launch_attend_wide(codes, p, a, stream, &err) : launch_attend(p, a, stream, &err))
+    return fail(QKNORM_ERR_HIP, "%s: %s", fn, err.c_str());
   return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int qknorm_headwise_rope(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype, float eps,
+                         int64_t head_dim, int64_t gamma_head_stride, const qknorm_rope_t* rope, void* stream) {
+  return rope_forward("qknorm_headwise_rope", q, k, T, dtype, eps, head_dim, gamma_head_stride, rope, nullptr, stream);
+}
+
+int qknorm_headwise_rope_axes(const qknorm_operand_t* q, const qknorm_operand_t* k, int64_t T, int dtype, float eps,
+                              int64_t head_dim, int64_t gamma_head_stride, const qknorm_rope_t* rope,
+                              const qknorm_axes_t* axes, void* stream) {
+  return rope_forward("qknorm_headwise_rope_axes", q, k, T, dtype, eps, head_dim, gamma_head_stride, rope, axes, stream);
+}
+
+int qknorm_headwise_rope_backward(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T,
+                                  int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                                  const qknorm_rope_t* rope, void* workspace, size_t workspace_bytes, void* stream) {
+  return rope_backward("qknorm_headwise_rope_backward", q, k, T, dtype, eps, head_dim, gamma_head_stride, rope, nullptr,
+                       workspace, workspace_bytes, stream);
+}
+
+int qknorm_headwise_rope_axes_backward(const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T,
+                                       int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                                       const qknorm_rope_t* rope, const qknorm_axes_t* axes, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  return rope_backward("qknorm_headwise_rope_axes_backward", q, k, T, dtype, eps, head_dim, gamma_head_stride, rope,
+                       axes, workspace, workspace_bytes, stream);
+}
+
+size_t qknorm_headwise_rope_backward_workspace(int64_t hq, int64_t hk, int64_t T, int dtype, int64_t head_dim,
+                                               int64_t gamma_head_stride) {
+  if (T <= 0 || head_dim <= 0 || head_dim > kRopeMaxHead || hq <= 0 || hk <= 0 || hq % head_dim || hk % head_dim ||
+      hq > kMaxWidth || hk > kMaxWidth || (dtype != QKNORM_F32 && dtype != QKNORM_BF16) || gamma_head_stride < 0)
+    return 0;
+  return grad_workspace(hq / head_dim, hk / head_dim, T, dtype, head_dim, gamma_head_stride);
+}
+
+int qknorm_paged_append(const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
+                        int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride, const qknorm_rope_t* rope,
+                        const qknorm_cache_t* cache, const int64_t* slots, void* stream) {
+  return append("qknorm_paged_append", q, k, v, T, dtype, eps, head_dim, gamma_head_stride, rope, nullptr, cache, slots,
+                stream);
+}
+
+int qknorm_paged_append_axes(const qknorm_operand_t* q, const qknorm_operand_t* k, const qknorm_operand_t* v, int64_t T,
+                             int dtype, float eps, int64_t head_dim, int64_t gamma_head_stride,
+                             const qknorm_rope_t* rope, const qknorm_axes_t* axes, const qknorm_cache_t* cache,
+                             const int64_t* slots, void* stream) {
+  return append("qknorm_paged_append_axes", q, k, v, T, dtype, eps, head_dim, gamma_head_stride, rope, axes, cache,
+                slots, stream);
+}
+
+int qknorm_paged_gather(const qknorm_cache_t* cache, int64_t head_dim, const int64_t* slots, int64_t T, int dtype,
+                        void* k_rows, int64_t ld_k, void* v_rows, int64_t ld_v, void* stream) {
+  return gather("qknorm_paged_gather", cache, head_dim, slots, T, dtype, k_rows, ld_k, v_rows, ld_v, stream);
+}
+
+int qknorm_paged_attend(const qknorm_operand_t* q, int64_t T, int dtype, const qknorm_cache_t* cache,
+                        int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return attend("qknorm_paged_attend", false, q, T, dtype, cache, head_dim, batch, scale, causal, window, workspace,
+                workspace_bytes, stream);
+}
+
+int qknorm_paged_attend_wide(const qknorm_operand_t* q, int64_t T, int dtype, const qknorm_cache_t* cache,
+                             int64_t head_dim, const qknorm_batch_t* batch, float scale, int causal, int64_t window,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  return attend("qknorm_paged_attend_wide", true, q, T, dtype, cache, head_dim, batch, scale, causal, window,
+                workspace, workspace_bytes, stream);
 }
 
 size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
@@ -822,6 +1052,13 @@ size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k
   if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
   return attend_workspace(plan_attend(head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0),
                           T, heads_q);
+}
+
+size_t qknorm_paged_attend_wide_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
+                                          int64_t max_q, int64_t max_len) {
+  if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
+  return attend_workspace(
+      plan_attend_wide(head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0), T, heads_q);
 }
 
 }  // extern "C"

@@ -26,6 +26,7 @@
 #include "qknorm_rope_device.hpp"
 
 #include <string>
+#include <type_traits>
 
 namespace qkn {
 namespace {
@@ -81,10 +82,12 @@ struct Chunk1 {
 // cos and sin for a lane's chunk at one position (half-split: the sine with
 // the sign its member takes). A position outside the table gives NaN, which
 // reaches every rotated column of the token.
-template <int VW, bool INTER>
+// AXES: positions on several axes, each angle from the row of its own.
+template <int VW, bool INTER, bool AXES>
 struct Turn {
   static constexpr int TW = Chunk1<VW, INTER>::TW;
   float c[TW], s[TW];
+  uint32_t lost;     // AXES: bits of the angles that are NaN
   bool in;
   __device__ __forceinline__ void load(const float* table, int64_t ld, int64_t n, int64_t pos, int half, int tab) {
     in = pos >= 0 && pos < n;
@@ -92,8 +95,23 @@ struct Turn {
     load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + tab), reinterpret_cast<uint32_t*>(c));
     load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + half + tab), reinterpret_cast<uint32_t*>(s));
   }
+  template <class Args>
+  __device__ __forceinline__ void load(const Args& a, const Position<AXES>& pos, const Chunk1<VW, INTER>& at,
+                                       uint32_t axes) {
+    if constexpr (AXES)
+      lost = load_angles<TW>(axis_rows(a, pos), a.axes.mixed, axes, a.rot >> 1, at.tab, c, s);
+    else
+      load(a.cos_sin, a.ld_table, a.n_positions, pos.on[0], a.rot >> 1, at.tab);
+  }
   __device__ __forceinline__ void settle(const Chunk1<VW, INTER>& at) {
-    if (!in) {
+    if constexpr (AXES) {
+      if (__builtin_amdgcn_ballot_w64(lost != 0) != 0) {
+        keep_branch();
+#pragma unroll
+        for (int e = 0; e < TW; ++e)
+          if (lost >> e & 1) c[e] = s[e] = __builtin_nanf("");
+      }
+    } else if (!in) {
       keep_branch();
 #pragma unroll
       for (int e = 0; e < TW; ++e) c[e] = s[e] = __builtin_nanf("");
@@ -108,8 +126,8 @@ struct Turn {
 // Rotates a lane's chunk (BACK: by the opposite angle, the transposed map that
 // gradients take). half_lanes: lanes between the members of a pair. With MAG,
 // `mag` gets the magnitudes that each result is the sum of.
-template <bool BACK, bool MAG, class F, int VW, bool INTER>
-__device__ __forceinline__ void rotate_chunk(F (&z)[VW], const Turn<VW, INTER>& t, const Chunk1<VW, INTER>& at,
+template <bool BACK, bool MAG, class F, int VW, bool INTER, bool AXES>
+__device__ __forceinline__ void rotate_chunk(F (&z)[VW], const Turn<VW, INTER, AXES>& t, const Chunk1<VW, INTER>& at,
                                              int half_lanes, bool partial, float (&mag)[VW]) {
   F y[VW], p[VW];
   if constexpr (INTER) {
@@ -146,10 +164,7 @@ __device__ __forceinline__ void rotate_chunk(F (&z)[VW], const Turn<VW, INTER>& 
   for (int e = 0; e < VW; ++e) z[e] = partial && !at.turned ? z[e] : y[e];
 }
 
-// MXFP4: per 32 channels the scale 2^E with E = floor(log2(largest)) - 2 held
-// to [-100, 125], and E2M1 codes rounded to nearest even, magnitudes past 6
-// saturating. 32 / VW lanes hold a block. One that holds an infinity or NaN
-// gets the scale byte 0xFF and reads as NaN.
+// The largest over the 32 / VW lanes that hold a block.
 template <int VW>
 __device__ __forceinline__ uint32_t block_max(uint32_t m) {
   m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
@@ -157,51 +172,33 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
   if (VW == 4) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
   return m;
 }
-// The scale byte of a block whose largest magnitude has these bits (NaN above infinity).
-__device__ __forceinline__ int scale_byte(uint32_t m) {
-  return m >= 0x7F800000u ? 0xFF : min(max((int)(m >> 23) - 2, 27), 252);
-}
-__device__ __forceinline__ float over_scale(int byte) {   // 2^-E
-  return __uint_as_float((uint32_t)(254 - (byte == 0xFF ? 127 : byte)) << 23);
-}
-template <int VW>
-__device__ __forceinline__ uint32_t codes_of(const float (&a)[VW]) {   // already over the scale
-  uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[0], a[1], 1.0f, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[2], a[3], 1.0f, 1);
-  if constexpr (VW == 8) {
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[4], a[5], 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[6], a[7], 1.0f, 3);
-  }
-  return w;
-}
+template <class MX, int VW>
 struct Coded {
-  uint32_t w;
+  Codes<MX, VW> codes;
   int byte;
 };
 
 // The codes of a lane's values.
-template <int VW>
-__device__ __forceinline__ Coded quantize(const float (&f)[VW]) {
+template <class MX, int VW>
+__device__ __forceinline__ Coded<MX, VW> quantize(const float (&f)[VW]) {
   uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < VW; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-  Coded q;
-  q.byte = scale_byte(block_max<VW>(m));
+  Coded<MX, VW> q;
+  q.byte = scale_byte<MX>(block_max<VW>(m));
   const float inv = over_scale(q.byte);
   float a[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) a[e] = q.byte == 0xFF ? 0.0f : f[e] * inv;
-  q.w = codes_of<VW>(a);
+  q.codes = codes_of<MX, VW>(a);
   return q;
 }
 
 // The codes of values known to within kUnsure of `mag`: true if every value
 // within that distance has them (in this lane's share of its block).
 constexpr float kUnsure = 0x1p-19f;
-constexpr float kMostFactor = 0x1p24f;   // largest RMS factor for which that distance holds
-template <int VW>
-__device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float (&mag)[VW], Coded& q) {
+template <class MX, int VW>
+__device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float (&mag)[VW], Coded<MX, VW>& q) {
   float lo[VW], hi[VW];
   uint32_t ml = 0, mh = 0;
 #pragma unroll
@@ -215,23 +212,24 @@ __device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float 
   }
   ml = block_max<VW>(ml);
   mh = block_max<VW>(mh);
-  q.byte = scale_byte(mh);
-  if (mh >= 0x7F800000u || scale_byte(ml) != q.byte) return false;
+  q.byte = scale_byte<MX>(mh);
+  if (mh >= 0x7F800000u || scale_byte<MX>(ml) != q.byte) return false;
   const float inv = over_scale(q.byte);
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
     hi[e] = __builtin_copysignf(hi[e] * inv, f[e]);
     lo[e] = __builtin_copysignf(lo[e] * inv, f[e]);
   }
-  q.w = codes_of<VW>(hi);
-  return q.w == codes_of<VW>(lo);
+  q.codes = codes_of<MX, VW>(hi);
+  return q.codes == codes_of<MX, VW>(lo);
 }
 
 // A lane's normalized and rotated chunk formed in float64 and rounded to odd,
 // four elements at a time to keep registers for waves.
-template <class IO, bool INTER>
-__device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, const char* gamma, int64_t pos, bool turns,
-                                            const Chunk1<IO::kVW, INTER>& at, int L, float (&f)[IO::kVW]) {
+template <class IO, bool INTER, bool AXES>
+__device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, const char* gamma, const Position<AXES>& pos, bool turns,
+                                            const Chunk1<IO::kVW, INTER>& at, uint32_t axes, int L,
+                                            float (&f)[IO::kVW]) {
   constexpr int VW = IO::kVW;
   constexpr int GB = VW * IO::kGBytes;
   float v[VW], g[VW];
@@ -253,8 +251,17 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
     ss = group_sum_d(ss, L);
     r = 1.0 / __builtin_sqrt(ss / a.head_dim + (double)a.eps);
   }
-  const bool in = pos >= 0 && pos < a.n_positions;
-  const float* row = turns ? a.cos_sin + (in ? pos : 0) * a.ld_table + at.tab : nullptr;
+  bool in = false;
+  const float* row = nullptr;
+  AxisRows rows;
+  if (turns) {
+    if constexpr (AXES) {
+      rows = axis_rows(a, pos);
+    } else {
+      in = pos.on[0] >= 0 && pos.on[0] < a.n_positions;
+      row = a.cos_sin + (in ? pos.on[0] : 0) * a.ld_table + at.tab;
+    }
+  }
 #pragma unroll 1
   for (int e0 = 0; e0 < VW; e0 += 4) {
     double z[4], p[4];
@@ -281,6 +288,11 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = INTER ? (e0 + k) >> 1 : e0 + k;
+        if constexpr (AXES) {
+          const uint32_t axis = axes >> (2 * i) & 3;
+          row = rows.of(axis) + at.tab;
+          in = rows.in >> axis & 1;
+        }
         const double c = in ? row[i] : __builtin_nanf(""), sn = in ? row[(a.rot >> 1) + i] : __builtin_nanf("");
         const bool first = INTER ? (k & 1) == 0 : at.flip != 0;   // of its pair: the sine is subtracted
         const double y = z[k] * c + p[k] * (first ? -sn : sn);
@@ -301,20 +313,6 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
   }
 }
 
-// The values that codes stand for.
-template <int VW>
-__device__ __forceinline__ void coded_values(const Coded& q, float (&f)[VW]) {
-  const float back = __uint_as_float(q.byte == 0xFF ? 0x7FC00000u : (uint32_t)q.byte << 23);
-  const f32x2_t y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 0);
-  const f32x2_t y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 1);
-  f[0] = y0[0] * back, f[1] = y0[1] * back, f[2] = y1[0] * back, f[3] = y1[1] * back;
-  if constexpr (VW == 8) {
-    const f32x2_t y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 2);
-    const f32x2_t y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w, 1.0f, 3);
-    f[4] = y2[0] * back, f[5] = y2[1] * back, f[6] = y3[0] * back, f[7] = y3[1] * back;
-  }
-}
-
 // The forward pass (MODE ROPE_FORWARD: Q and K rows to y) and the append
 // calls (Q to y, K and V into the cache). A wave takes one token's next S
 // slots of one side; which, its number says (a.groups waves per token). All of
@@ -327,9 +325,11 @@ __device__ __forceinline__ void coded_values(const Coded& q, float (&f)[VW]) {
 // Apart, because one kernel for both took the registers of the longer one:
 // 70 us. The paired layout is faster only for a cache of rows and about a
 // thousand tokens (10.7 us against 11.7).
-template <class IO, int S, bool INTER, int MODE>
+template <class IO, int S, bool INTER, int MODE, bool AXES>
 __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeArgs a) {
   constexpr int VW = IO::kVW;
+  constexpr bool CODES = MODE == ROPE_APPEND_MXFP4 || MODE == ROPE_APPEND_MXFP8;
+  using MX = std::conditional_t<MODE == ROPE_APPEND_MXFP8, Mx8, Mx4>;
   constexpr int GB = VW * IO::kGBytes;
   constexpr uint32_t XR = 16;
   const int lane = threadIdx.x & 63;
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
   const Chunk1<VW, INTER> at(lane & (L - 1), a.rot, a.half_lanes);
   const bool partial = a.rot < a.head_dim;
   const bool turns = a.rot != 0 && c != 2;
+  const uint32_t axes = AXES ? axes_at(a.axes, at.tab) : 0;
 
   const char* gamma = static_cast<const char*>(c == 2 ? nullptr : o.gamma);
   Piece<GB> gam;   // of the first slot: of all where heads share it
@@ -363,18 +364,18 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
   }
 
   // Slot i's results (codes in q, for a cache of them) to where they go.
-  const auto store = [&](int i, bool on, float (&f)[VW], const Coded& q, int64_t t, int64_t place) {
+  const auto store = [&](int i, bool on, float (&f)[VW], const Coded<MX, VW>& q, int64_t t, int64_t place) {
     const int64_t head = head0 + i * hw;
     if (MODE != ROPE_FORWARD && c != 0) {
       const int64_t page = place >> a.log2_page, in = place & (((int64_t)1 << a.log2_page) - 1);
       char* p = a.cache[c - 1] + page * a.page_stride + in * a.token_stride + head * a.head_stride;
-      if constexpr (MODE == ROPE_APPEND_MXFP4) {
+      if constexpr (CODES) {
         char* sc = a.scales[c - 1] + page * a.scale_page_stride + in * (a.head_dim >> 5) + head * a.scale_head_stride;
         if (on) {
-          store_bytes<VW / 2>(p + (at.col >> 1), &q.w);
+          store_bytes<VW * MX::kBits / 8>(p + at.col * MX::kBits / 8, q.codes.w);
           if ((lane & (32 / VW - 1)) == 0) sc[at.col >> 5] = (char)q.byte;
         }
-        if (o.y) coded_values<VW>(q, f);
+        if (o.y) code_values<MX, VW>(q.codes, q.byte, f);
       } else {
         Piece<16> w;
         narrow<IO, VW>(f, w.w);
@@ -392,16 +393,17 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
     uint32_t unsure = 0;   // slots whose codes float32 leaves open
     // A row that holds no token is worked like the others, and not stored: its
     // slot, waited for first, would hold up all that follows.
-    int64_t place = 0, pos = 0;
+    int64_t place = 0;
+    Position<AXES> pos;
     if constexpr (MODE != ROPE_FORWARD) place = load_uniform(a.slots + t);
-    if (turns) pos = load_uniform(a.positions + t);
+    if (turns) pos.load(a, t);
     Piece<16> x[S];
 #pragma unroll
     for (int i = 0; i < S; ++i)
       load_bytes<16, true>(static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + off[i], x[i].w);
-    Turn<VW, INTER> turn;
+    Turn<VW, INTER, AXES> turn;
     if (turns) {
-      turn.load(a.cos_sin, a.ld_table, a.n_positions, pos, a.rot >> 1, at.tab);
+      turn.load(a, pos, at, axes);
       turn.settle(at);
     }
     const bool live = MODE == ROPE_FORWARD || (place >= 0 && place < a.n_tokens_held);
@@ -422,24 +424,24 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
         for (int e = 0; e < VW; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
         ss = group_sum(ss, L);
         const float r = rms_factor(ss, a.inv_div, a.eps);
-        ranged = r > 0.0f && r <= kMostFactor;
+        ranged = r > 0.0f && r <= MX::kMostFactor;
         float g[VW];
         widen_gamma<IO, VW>(gam.w, g);
 #pragma unroll
         for (int e = 0; e < VW; ++e) f[e] = (f[e] * g[e]) * r;
       }
-      if (MODE == ROPE_APPEND_MXFP4) {
+      if (CODES) {
 #pragma unroll
         for (int e = 0; e < VW; ++e) mag[e] = __builtin_fabsf(f[e]);
       }
-      if (turns) rotate_chunk<false, MODE == ROPE_APPEND_MXFP4>(f, turn, at, a.half_lanes, partial, mag);
+      if (turns) rotate_chunk<false, CODES>(f, turn, at, a.half_lanes, partial, mag);
 
-      Coded q;
-      if (MODE == ROPE_APPEND_MXFP4 && c != 0) {
+      Coded<MX, VW> q;
+      if (CODES && c != 0) {
         if (c == 2) {
-          q = quantize<VW>(f);
+          q = quantize<MX, VW>(f);
         } else {
-          const bool sure = quantize_sure<VW>(f, mag, q);
+          const bool sure = quantize_sure<MX, VW>(f, mag, q);
           if (__builtin_amdgcn_ballot_w64(!(sure && ranged)) != 0) {
             unsure |= 1u << i;
             continue;
@@ -449,14 +451,14 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
       store(i, on && live, f, q, t, place);
     }
 
-    if constexpr (MODE == ROPE_APPEND_MXFP4) {
+    if constexpr (CODES) {
       // A key's float32 value is within 16 u of the magnitudes it is the sum
       // of (r within 11 u: a chain of 8 squares, 6 butterfly adds, the factor;
       // then 4 roundings), u = 2^-24; kUnsure is twice that. It is so where the
       // sum is finite (r > 0) and subnormal roundings, of 2^-150 at most, count
       // for nothing: with r up to 2^24 they are below u of the mean square, and
-      // below kUnsure / 16 of the lowest border there is, 2^-102. Where a border
-      // of the codes or of the scale lies that near to one (in about 2% of the
+      // below kUnsure / 16 of the lowest border there is, 2^-102 (8 bits: 2^16 and
+      // 2^-110). Where a border of the codes or of the scale lies that near to one (in 2 or 3% of the
       // slots), or r is out of that range, the slot is formed again in float64,
       // so that every code is the one exact arithmetic gives and does not hang
       // on the order of a sum.
@@ -468,11 +470,11 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
         const int head = head0 + i * hw;
         const bool on = head < o.heads;
         float f[VW];
-        exact_chunk<IO, INTER>(
+        exact_chunk<IO, INTER, AXES>(
             a, static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + (int64_t)((on ? head : 0) * a.head_dim + at.col) * IO::kBytes,
             gamma ? gamma + ((on ? head : 0) * a.gstride + at.col) * IO::kGBytes : nullptr,
-            pos, turns, at, L, f);
-        const Coded q = quantize<VW>(f);
+            pos, turns, at, axes, L, f);
+        const Coded<MX, VW> q = quantize<MX, VW>(f);
         store(i, on, f, q, t, place);
       }
     }
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
 // issued before the current one is worked on. 8192 tokens x 48 heads x 128
 // bf16 columns: 59.5 us with the sums (56 and 5 traced one by one), 5.1 TB/s
 // where a copy of one stream reaches 6.06; 32 float32 heads 72.9 us, 5.6 TB/s.
-template <class IO, bool INTER>
+template <class IO, bool INTER, bool AXES>
 __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGradArgs a) {
   constexpr int VW = IO::kVW;
   constexpr int GB = VW * IO::kGBytes;
@@ -508,6 +510,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
   const int hc = on ? head : 0;
   const Chunk1<VW, INTER> at(lane & (L - 1), a.rot, a.half_lanes);
   const bool partial = a.rot < a.head_dim;
+  const uint32_t axes = AXES ? axes_at(a.axes, at.tab) : 0;
   const uint32_t off = (uint32_t)(hc * a.head_dim + at.col) * IO::kBytes;
 
   float g[VW], sum[VW];
@@ -521,13 +524,16 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
 
   struct In {
     Piece<16> x, dy;
-    Turn<VW, INTER> turn;
+    Turn<VW, INTER, AXES> turn;
   };
   const auto load = [&](In& in, int64_t t) {
     load_bytes<16, true>(static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + off, in.x.w);
     load_bytes<16, true>(static_cast<const char*>(o.dy) + t * o.lddy * IO::kBytes + off, in.dy.w);
-    if (a.rot)
-      in.turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at.tab);
+    if (a.rot) {
+      Position<AXES> pos;
+      pos.load(a, t);
+      in.turn.load(a, pos, at, axes);
+    }
   };
   const auto work = [&](In& in, int64_t t) {
     float x[VW], y[VW], gg[VW];
@@ -616,43 +622,55 @@ __global__ void __launch_bounds__(1024) qknorm_rope_grad_sum(const RopeGradArgs 
   }
 }
 
-template <class IO, bool INTER, int MODE>
+template <class IO, bool INTER, int MODE, bool AXES>
 const void* pick_slots(int slots) {
   switch (slots) {
-    case 1: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 1, INTER, MODE>);
-    case 2: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 2, INTER, MODE>);
-    case 3: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 3, INTER, MODE>);
-    case 4: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 4, INTER, MODE>);
+    case 1: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 1, INTER, MODE, AXES>);
+    case 2: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 2, INTER, MODE, AXES>);
+    case 3: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 3, INTER, MODE, AXES>);
+    case 4: return reinterpret_cast<const void*>(qknorm_rope_rows<IO, 4, INTER, MODE, AXES>);
   }
   return nullptr;
 }
 
-template <class IO, bool INTER>
+template <class IO, bool INTER, bool AXES>
 const void* pick_mode(int mode, int slots) {
-  if (mode == ROPE_FORWARD) return pick_slots<IO, INTER, ROPE_FORWARD>(slots);
+  if (mode == ROPE_FORWARD) return pick_slots<IO, INTER, ROPE_FORWARD, AXES>(slots);
   if constexpr (IO::kBytes > 1) {
-    if (mode == ROPE_APPEND_ROWS) return pick_slots<IO, INTER, ROPE_APPEND_ROWS>(slots);
-    return pick_slots<IO, INTER, ROPE_APPEND_MXFP4>(slots);
+    if (mode == ROPE_APPEND_ROWS) return pick_slots<IO, INTER, ROPE_APPEND_ROWS, AXES>(slots);
+    if (mode == ROPE_APPEND_MXFP8) return pick_slots<IO, INTER, ROPE_APPEND_MXFP8, AXES>(slots);
+    return pick_slots<IO, INTER, ROPE_APPEND_MXFP4, AXES>(slots);
   }
   return nullptr;
 }
 
-const void* rope_kernel(int mode, int dtype, bool inter, const RopePlan& p) {
-  if (!p.whole) return rope_paired_kernel(mode, dtype, inter, p);
+template <class IO>
+const void* pick_turn(int mode, bool inter, bool axes, int slots) {
+  if (axes) return inter ? pick_mode<IO, true, true>(mode, slots) : pick_mode<IO, false, true>(mode, slots);
+  return inter ? pick_mode<IO, true, false>(mode, slots) : pick_mode<IO, false, false>(mode, slots);
+}
+
+const void* rope_kernel(int mode, int dtype, bool inter, bool axes, const RopePlan& p) {
+  if (!p.whole) return rope_paired_kernel(mode, dtype, inter, axes, p);
   switch (dtype) {
-    case kDtypeBF16: return inter ? pick_mode<BF16, true>(mode, p.slots) : pick_mode<BF16, false>(mode, p.slots);
-    case kDtypeF32: return inter ? pick_mode<F32, true>(mode, p.slots) : pick_mode<F32, false>(mode, p.slots);
-    default: return inter ? pick_mode<FP8, true>(mode, p.slots) : pick_mode<FP8, false>(mode, p.slots);
+    case kDtypeBF16: return pick_turn<BF16>(mode, inter, axes, p.slots);
+    case kDtypeF32: return pick_turn<F32>(mode, inter, axes, p.slots);
+    default: return pick_turn<FP8>(mode, inter, axes, p.slots);
   }
 }
 
-const void* rope_grad_kernel(int dtype, bool inter, const RopePlan& p) {
-  if (!p.whole) return rope_paired_grad_kernel(dtype, inter, p);
-  if (dtype == kDtypeBF16)
-    return inter ? reinterpret_cast<const void*>(qknorm_rope_grad<BF16, true>)
-                 : reinterpret_cast<const void*>(qknorm_rope_grad<BF16, false>);
-  return inter ? reinterpret_cast<const void*>(qknorm_rope_grad<F32, true>)
-               : reinterpret_cast<const void*>(qknorm_rope_grad<F32, false>);
+template <class IO>
+const void* pick_grad_turn(bool inter, bool axes) {
+  if (axes)
+    return inter ? reinterpret_cast<const void*>(qknorm_rope_grad<IO, true, true>)
+                 : reinterpret_cast<const void*>(qknorm_rope_grad<IO, false, true>);
+  return inter ? reinterpret_cast<const void*>(qknorm_rope_grad<IO, true, false>)
+               : reinterpret_cast<const void*>(qknorm_rope_grad<IO, false, false>);
+}
+
+const void* rope_grad_kernel(int dtype, bool inter, bool axes, const RopePlan& p) {
+  if (!p.whole) return rope_paired_grad_kernel(dtype, inter, axes, p);
+  return dtype == kDtypeBF16 ? pick_grad_turn<BF16>(inter, axes) : pick_grad_turn<F32>(inter, axes);
 }
 
 int launched(hipError_t e, std::string* err) {
@@ -666,7 +684,7 @@ int launched(hipError_t e, std::string* err) {
 constexpr int64_t kRopeMostBlocks = (int64_t)1 << 22;
 
 static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeArgs a, void* stream, std::string* err) {
-  const void* fn = rope_kernel(mode, dtype, inter, p);
+  const void* fn = rope_kernel(mode, dtype, inter, a.axes.n > 0, p);
   if (!fn) {
     *err = "no kernel compiled for this plan";
     return (int)hipErrorInvalidValue;
@@ -718,7 +736,7 @@ int64_t rope_grad_rows(const RopeGradArgs& a) {
 
 int launch_rope_grad(int dtype, bool inter, const RopePlan& p, const RopeGradArgs& args, void* stream,
                      std::string* err) {
-  const void* fn = rope_grad_kernel(dtype, inter, p);
+  const void* fn = rope_grad_kernel(dtype, inter, args.axes.n > 0, p);
   RopeGradArgs a = args;
   void* kargs[] = {&a};
   const int rc = launched(hipLaunchKernel(fn,

@@ -141,6 +141,148 @@ __device__ __forceinline__ void narrow(const float (&v)[VW], uint32_t* w) {
   }
 }
 
+// The rows of the angle table that a token's positions on several axes name,
+// the same for the whole wave. A position outside the table reads row 0, and its
+// angles become NaN.
+struct AxisRows {
+  uint64_t row0, row1, row2, row3;   // (an array would be chosen from in memory)
+  uint32_t in;                       // bit x: the position on axis x lies in the table
+  __device__ __forceinline__ const float* of(uint32_t axis) const {
+    const uint64_t lo = axis & 1 ? row1 : row0, hi = axis & 1 ? row3 : row2;
+    return reinterpret_cast<const float*>(axis & 2 ? hi : lo);
+  }
+};
+static_assert(kMostAxes == 4, "AxisRows");
+// A token's position, or AXES: its positions (axes there are not: the first).
+template <bool AXES>
+struct Position {
+  int64_t on[AXES ? kMostAxes : 1];
+  template <class Args>
+  __device__ __forceinline__ void load(const Args& a, int64_t t) {
+    on[0] = load_uniform(a.positions + t);
+    if constexpr (AXES) {
+#pragma unroll
+      for (int x = 1; x < kMostAxes; ++x) on[x] = load_uniform(a.positions + (x < a.axes.n ? x : 0) * a.axes.ld + t);
+    }
+  }
+};
+template <class Args>
+__device__ __forceinline__ AxisRows axis_rows(const Args& a, const Position<true>& pos) {
+  AxisRows r;
+  r.in = 0;
+  const auto row = [&](int x) {
+    const bool in = pos.on[x] >= 0 && pos.on[x] < a.n_positions;
+    r.in |= (uint32_t)in << x;
+    return uniform64(reinterpret_cast<uint64_t>(a.cos_sin + (in ? pos.on[x] : 0) * a.ld_table));
+  };
+  r.row0 = row(0), r.row1 = row(1), r.row2 = row(2), r.row3 = row(3);
+  return r;
+}
+// The axes of the angles from `tab` on, two bits each (a piece's angles share a word).
+__device__ __forceinline__ uint32_t axes_at(const RopeAxes& axes, int tab) {
+  return axes.of[tab >> 4] >> (2 * (tab & 15));
+}
+// cos and sin of N angles from `tab` on, each from the row of its axis, with wide
+// loads where they share one. Returns a bit for each angle of a position outside
+// the table.
+template <int N>
+__device__ __forceinline__ uint32_t load_angles(const AxisRows& rows, bool mixed, uint32_t axes, int half, int tab,
+                                                float (&c)[N], float (&s)[N]) {
+  if (!mixed) {
+    const float* row = rows.of(axes & 3) + tab;
+    load_bytes<N * 4, false>(reinterpret_cast<const char*>(row), reinterpret_cast<uint32_t*>(c));
+    load_bytes<N * 4, false>(reinterpret_cast<const char*>(row + half), reinterpret_cast<uint32_t*>(s));
+    return rows.in >> (axes & 3) & 1 ? 0u : ~0u;
+  }
+  uint32_t lost = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const uint32_t axis = axes >> (2 * e) & 3;
+    const float* row = rows.of(axis) + tab + e;
+    c[e] = row[0];
+    s[e] = row[half];
+    lost |= (~rows.in >> axis & 1) << e;
+  }
+  return lost;
+}
+
+// The formats of quantised caches. A block of 32 channels has the scale 2^E, E =
+// floor(log2(largest magnitude)) - kLead held to [-100, kTop - 127], and codes
+// rounded to nearest even, magnitudes past the largest code's saturating. One
+// that holds an infinity or NaN gets codes 0 and the scale byte 0xFF and reads as
+// NaN. kMostFactor: see qknorm_rope_rows.
+struct Mx4 {   // E2M1
+  static constexpr int kBits = 4, kLead = 2, kTop = 252;
+  static constexpr float kMostFactor = 0x1p24f;
+};
+struct Mx8 {   // E4M3
+  static constexpr int kBits = 8, kLead = 8, kTop = 246;
+  static constexpr float kMostFactor = 0x1p16f;
+};
+
+// The scale byte of a block whose largest magnitude has these bits (NaN above infinity).
+template <class MX>
+__device__ __forceinline__ int scale_byte(uint32_t m) {
+  return m >= 0x7F800000u ? 0xFF : min(max((int)(m >> 23) - MX::kLead, 27), MX::kTop);
+}
+__device__ __forceinline__ float over_scale(int byte) {   // 2^-E
+  return __uint_as_float((uint32_t)(254 - (byte == 0xFF ? 127 : byte)) << 23);
+}
+template <class MX, int VW>
+struct Codes {
+  uint32_t w[VW * MX::kBits / 32 > 0 ? VW * MX::kBits / 32 : 1];
+  __device__ __forceinline__ bool operator==(const Codes& o) const {
+    bool same = true;
+#pragma unroll
+    for (uint32_t i = 0; i < sizeof(w) / 4; ++i) same = same && w[i] == o.w[i];
+    return same;
+  }
+};
+// The codes of values already over the scale.
+template <class MX, int VW>
+__device__ __forceinline__ Codes<MX, VW> codes_of(const float (&a)[VW]) {
+  Codes<MX, VW> q;
+  if constexpr (MX::kBits == 4) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[0], a[1], 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[2], a[3], 1.0f, 1);
+    if constexpr (VW == 8) {
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[4], a[5], 1.0f, 2);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[6], a[7], 1.0f, 3);
+    }
+    q.w[0] = w;
+  } else {
+    float v[VW];   // finite: scaled values are below 512, and a block with others has none
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = __builtin_amdgcn_fmed3f(a[e], -448.0f, 448.0f);
+#pragma unroll
+    for (int p = 0; p < VW / 4; ++p) q.w[p] = pack_fp8_word(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+  }
+  return q;
+}
+// The values that codes with a scale byte stand for (exact).
+template <class MX, int VW>
+__device__ __forceinline__ void code_values(const Codes<MX, VW>& q, int byte, float (&f)[VW]) {
+  const float back = __uint_as_float(byte == 0xFF ? 0x7FC00000u : (uint32_t)byte << 23);
+  if constexpr (MX::kBits == 4) {
+    const f32x2_t y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w[0], 1.0f, 0);
+    const f32x2_t y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w[0], 1.0f, 1);
+    f[0] = y0[0] * back, f[1] = y0[1] * back, f[2] = y1[0] * back, f[3] = y1[1] * back;
+    if constexpr (VW == 8) {
+      const f32x2_t y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w[0], 1.0f, 2);
+      const f32x2_t y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w[0], 1.0f, 3);
+      f[4] = y2[0] * back, f[5] = y2[1] * back, f[6] = y3[0] * back, f[7] = y3[1] * back;
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < VW / 4; ++p) {
+      const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(q.w[p], false);
+      const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8(q.w[p], true);
+      f[4 * p] = lo[0] * back, f[4 * p + 1] = lo[1] * back, f[4 * p + 2] = hi[0] * back, f[4 * p + 3] = hi[1] * back;
+    }
+  }
+}
+
 // A wave's tokens t, t + step, ...: each token's loads are issued before the
 // one before it is worked on, in two buffers that take turns. The loop loads
 // without a condition (past the last token, that one again): a branch around

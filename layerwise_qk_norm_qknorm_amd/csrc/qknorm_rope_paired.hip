@@ -17,6 +17,7 @@
 #include "qknorm_rope_device.hpp"
 
 #include <string>
+#include <type_traits>
 
 namespace qkn {
 namespace {
@@ -62,9 +63,34 @@ __device__ __forceinline__ void drop_idle(Piece<PB> (&a)[NP], Piece<PB> (&b)[NP]
 
 // cos and sin of the lane's pairs at one position. A position outside the
 // table gives NaN, which reaches every rotated column of the token.
-template <int VW, int NP, bool INTER>
+template <int VW, int NP, bool INTER, bool AXES>
 struct Angles {
   float c[NP][VW], s[NP][VW];
+  // of token t; AXES: positions on several axes, each angle from the row of its own
+  template <class Args>
+  __device__ __forceinline__ void load(const Args& a, int64_t t, const Place<VW, NP, INTER>& at) {
+    if constexpr (AXES) {
+      Position<true> pos;
+      pos.load(a, t);
+      const AxisRows rows = axis_rows(a, pos);
+      uint32_t lost[NP], any = 0;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        lost[k] = load_angles<VW>(rows, a.axes.mixed, axes_at(a.axes, at.tab[k]), a.rot >> 1, at.tab[k], c[k], s[k]);
+        any |= lost[k];
+      }
+      if (__builtin_amdgcn_ballot_w64(any != 0) != 0) {
+        keep_branch();
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+          for (int e = 0; e < VW; ++e)
+            if (lost[k] >> e & 1) c[k][e] = s[k][e] = __builtin_nanf("");
+      }
+    } else {
+      load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
+    }
+  }
   __device__ __forceinline__ void load(const float* table, int64_t ld, int64_t n, int64_t pos, int half,
                                        const Place<VW, NP, INTER>& at) {
     const bool in = pos >= 0 && pos < n;
@@ -113,12 +139,9 @@ __device__ __forceinline__ void rotate(F (&a)[VW], F (&b)[VW], const float (&c)[
 // Most float32 values of one slot's heads (one wave's exchange buffer).
 constexpr int kSlotValues = 1024;
 
-// One wave's slot of K or V values, float32 in `val` ([heads][head_dim]),
-// into MXFP4: per 32 channels the scale 2^E with E = floor(log2(largest)) - 2
-// held to [-100, 125], and E2M1 codes rounded to nearest even, magnitudes
-// past 6 saturating. Four lanes hold a block, eight channels each. A block
-// that holds an infinity or NaN gets the scale byte 0xFF and reads as NaN.
-template <class IO>
+// One wave's slot of K or V values, float32 in `val` ([heads][head_dim]), into
+// the codes of a quantised cache. Four lanes hold a block, eight channels each.
+template <class IO, class MX>
 __device__ __forceinline__ void quantize_slot(const float* val, const RopeArgs& a, int lane, int heads_here,
                                               int head0, char* codes, char* scales, char* y_row) {
   const int per_head = a.head_dim >> 3;   // eight-channel pieces
@@ -143,28 +166,17 @@ __device__ __forceinline__ void quantize_slot(const float* val, const RopeArgs& 
     for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
     m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
     m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
-    const bool bad = m >= 0x7F800000u;
-    const int byte = bad ? 0xFF : min(max((int)(m >> 23) - 2, 27), 252);
-    const float inv = __uint_as_float((uint32_t)(254 - (bad ? 127 : byte)) << 23);
-    uint32_t w = 0;
+    const int byte = scale_byte<MX>(m);
+    const float inv = over_scale(byte);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = bad ? 0.0f : f[e] * inv;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], 1.0f, 3);
+    for (int e = 0; e < 8; ++e) f[e] = byte == 0xFF ? 0.0f : f[e] * inv;
+    const Codes<MX, 8> w = codes_of<MX, 8>(f);
     if (on) {
-      *reinterpret_cast<uint32_t*>(codes + (int64_t)(head0 + h) * a.head_stride + (c >> 1)) = w;
+      store_bytes<MX::kBits>(codes + (int64_t)(head0 + h) * a.head_stride + c * MX::kBits / 8, w.w);
       if ((lane & 3) == 0) scales[(int64_t)(head0 + h) * a.scale_head_stride + (c >> 5)] = (char)byte;
       if (y_row) {   // what the cache now holds, in the row type (exact)
-        const float scale = __uint_as_float(bad ? 0x7FC00000u : (uint32_t)byte << 23);
         float y[8];
-        const f32x2_t y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-        const f32x2_t y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-        const f32x2_t y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-        const f32x2_t y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-        y[0] = y0[0] * scale, y[1] = y0[1] * scale, y[2] = y1[0] * scale, y[3] = y1[1] * scale;
-        y[4] = y2[0] * scale, y[5] = y2[1] * scale, y[6] = y3[0] * scale, y[7] = y3[1] * scale;
+        code_values<MX, 8>(w, byte, y);
         uint32_t o[IO::kBytes * 2];
         narrow<IO, 8>(y, o);
         char* p = y_row + ((int64_t)(head0 + h) * a.head_dim + c) * IO::kBytes;
@@ -188,11 +200,13 @@ __device__ __forceinline__ void quantize_slot(const float* val, const RopeArgs& 
 // each with S slots of it, `tokens` tokens; grid.y covers the slots past a
 // block's waves. All loads of a wave's slots are issued before the first is
 // used.
-template <class IO, int PB, int NP, int S, bool INTER, int MODE>
+template <class IO, int PB, int NP, int S, bool INTER, int MODE, bool AXES>
 __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const RopeArgs a) {
+  constexpr bool CODES = MODE == ROPE_APPEND_MXFP4 || MODE == ROPE_APPEND_MXFP8;
+  using MX = std::conditional_t<MODE == ROPE_APPEND_MXFP8, Mx8, Mx4>;
   constexpr int VW = PB / IO::kBytes;
   constexpr int GB = VW * IO::kGBytes;
-  __shared__ __align__(16) float exchange[MODE == ROPE_APPEND_MXFP4 ? kRopeMaxWaves * kSlotValues : 4];
+  __shared__ __align__(16) float exchange[CODES ? kRopeMaxWaves * kSlotValues : 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tok = (int)((uint32_t)wave * a.waves_inv >> 16);           // wave / waves
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
 
   struct In {   // one token
     Piece<PB> xa[S][NP], xb[S][NP];
-    Angles<VW, NP, INTER> turn;
+    Angles<VW, NP, INTER, AXES> turn;
     int64_t place;
   };
   const auto load = [&](In& in, int64_t t) {
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
         load_bytes<PB, true>(row + ob[i][k], in.xb[i][k].w);
       }
     }
-    if (a.rot_pairs) in.turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
+    if (a.rot_pairs) in.turn.load(a, t, at);
   };
 
   const auto work = [&](In& in, int64_t t) {
@@ -268,9 +282,9 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
         widen<IO, VW>(in.xa[i][k].w, fa[k]);
         widen<IO, VW>(in.xb[i][k].w, fb[k]);
       }
-      const bool exact = MODE == ROPE_APPEND_MXFP4 && c == 1;
+      const bool exact = CODES && c == 1;
       if (exact) {
-        // Keys bound for 4-bit codes: formed in float64 (vector float64 runs
+        // Keys bound for codes: formed in float64 (vector float64 runs
         // at the float32 rate here), so that every code is the one exact
         // arithmetic gives and does not hang on the order of a sum.
         double r = 1.0;
@@ -336,7 +350,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
       }
 
       char* y_row = o.y ? static_cast<char*>(o.y) + t * o.ldy * IO::kBytes : nullptr;
-      if (MODE == ROPE_APPEND_MXFP4 && c != 0) {
+      if (CODES && c != 0) {
         float* ex = exchange + wave * kSlotValues;
 #pragma unroll
         for (int k = 0; k < NP; ++k)
@@ -350,7 +364,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
         const int64_t page = in.place >> a.log2_page, off = in.place & (((int64_t)1 << a.log2_page) - 1);
         char* codes = a.cache[c - 1] + page * a.page_stride + off * a.token_stride;
         char* scales = a.scales[c - 1] + page * a.scale_page_stride + off * (a.head_dim >> 5);
-        quantize_slot<IO>(ex, a, lane, min(hw, o.heads - head0), head0, codes, scales, y_row);
+        quantize_slot<IO, MX>(ex, a, lane, min(hw, o.heads - head0), head0, codes, scales, y_row);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         continue;
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
 // LDS in a fixed order); qknorm_rope_grad_sum adds the rows in a fixed
 // order, so the gradients do not change from run to run. The next token's
 // loads are issued before the current one is worked on.
-template <class IO, int PB, int NP, bool INTER>
+template <class IO, int PB, int NP, bool INTER, bool AXES>
 __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(const RopeGradArgs a) {
   constexpr int VW = PB / IO::kBytes;
   constexpr int GB = VW * IO::kGBytes;
@@ -431,7 +445,7 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
 
   struct In {
     Piece<PB> xa[NP], xb[NP], ya[NP], yb[NP];
-    Angles<VW, NP, INTER> turn;
+    Angles<VW, NP, INTER, AXES> turn;
   };
   const auto load = [&](In& in, int64_t t) {
     const char* xr = x + t * o.ldx * IO::kBytes;
@@ -443,7 +457,7 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
       load_bytes<PB, true>(yr + oa[k], in.ya[k].w);
       load_bytes<PB, true>(yr + ob[k], in.yb[k].w);
     }
-    if (a.rot_pairs) in.turn.load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
+    if (a.rot_pairs) in.turn.load(a, t, at);
   };
   const auto work = [&](In& in, int64_t t) {
     if (a.idle) {
@@ -533,52 +547,63 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
 using RopeFn = void (*)(const RopeArgs);
 using GradFn = void (*)(const RopeGradArgs);
 
-template <class IO, bool INTER, int MODE>
+template <class IO, bool INTER, int MODE, bool AXES>
 RopeFn pick_rope(const RopePlan& p) {
   if (p.piece_bytes == 16) {
     switch (p.slots) {
-      case 1: return qknorm_rope_paired<IO, 16, 1, 1, INTER, MODE>;
-      case 3: return qknorm_rope_paired<IO, 16, 1, 3, INTER, MODE>;
+      case 1: return qknorm_rope_paired<IO, 16, 1, 1, INTER, MODE, AXES>;
+      case 3: return qknorm_rope_paired<IO, 16, 1, 3, INTER, MODE, AXES>;
     }
     return nullptr;
   }
   if (p.slots != 1) return nullptr;
-  if (p.piece_bytes == 8) return qknorm_rope_paired<IO, 8, 1, 1, INTER, MODE>;
-  if (p.np == 1) return qknorm_rope_paired<IO, IO::kBytes, 1, 1, INTER, MODE>;
-  return qknorm_rope_paired<IO, IO::kBytes, 8, 1, INTER, MODE>;
+  if (p.piece_bytes == 8) return qknorm_rope_paired<IO, 8, 1, 1, INTER, MODE, AXES>;
+  if (p.np == 1) return qknorm_rope_paired<IO, IO::kBytes, 1, 1, INTER, MODE, AXES>;
+  return qknorm_rope_paired<IO, IO::kBytes, 8, 1, INTER, MODE, AXES>;
 }
 
-template <class IO>
-RopeFn pick_rope_mode(int mode, bool inter, const RopePlan& p) {
-  if (mode == ROPE_FORWARD)
-    return inter ? pick_rope<IO, true, ROPE_FORWARD>(p) : pick_rope<IO, false, ROPE_FORWARD>(p);
+template <class IO, bool INTER, bool AXES>
+RopeFn pick_rope_mode(int mode, const RopePlan& p) {
+  if (mode == ROPE_FORWARD) return pick_rope<IO, INTER, ROPE_FORWARD, AXES>(p);
   if constexpr (IO::kBytes > 1) {
-    if (mode == ROPE_APPEND_ROWS)
-      return inter ? pick_rope<IO, true, ROPE_APPEND_ROWS>(p) : pick_rope<IO, false, ROPE_APPEND_ROWS>(p);
-    return inter ? pick_rope<IO, true, ROPE_APPEND_MXFP4>(p) : pick_rope<IO, false, ROPE_APPEND_MXFP4>(p);
+    if (mode == ROPE_APPEND_ROWS) return pick_rope<IO, INTER, ROPE_APPEND_ROWS, AXES>(p);
+    if (mode == ROPE_APPEND_MXFP8) return pick_rope<IO, INTER, ROPE_APPEND_MXFP8, AXES>(p);
+    return pick_rope<IO, INTER, ROPE_APPEND_MXFP4, AXES>(p);
   }
   return nullptr;
 }
 
-template <class IO, bool INTER>
+template <class IO>
+RopeFn pick_rope_turn(int mode, bool inter, bool axes, const RopePlan& p) {
+  if (axes) return inter ? pick_rope_mode<IO, true, true>(mode, p) : pick_rope_mode<IO, false, true>(mode, p);
+  return inter ? pick_rope_mode<IO, true, false>(mode, p) : pick_rope_mode<IO, false, false>(mode, p);
+}
+
+template <class IO, bool INTER, bool AXES>
 GradFn pick_grad(const RopePlan& p) {
-  if (p.piece_bytes == 16) return qknorm_rope_paired_grad<IO, 16, 1, INTER>;
-  if (p.piece_bytes == 8) return qknorm_rope_paired_grad<IO, 8, 1, INTER>;
-  if (p.np == 1) return qknorm_rope_paired_grad<IO, IO::kBytes, 1, INTER>;
-  return qknorm_rope_paired_grad<IO, IO::kBytes, 8, INTER>;
+  if (p.piece_bytes == 16) return qknorm_rope_paired_grad<IO, 16, 1, INTER, AXES>;
+  if (p.piece_bytes == 8) return qknorm_rope_paired_grad<IO, 8, 1, INTER, AXES>;
+  if (p.np == 1) return qknorm_rope_paired_grad<IO, IO::kBytes, 1, INTER, AXES>;
+  return qknorm_rope_paired_grad<IO, IO::kBytes, 8, INTER, AXES>;
+}
+
+template <class IO>
+GradFn pick_grad_turn(bool inter, bool axes, const RopePlan& p) {
+  if (axes) return inter ? pick_grad<IO, true, true>(p) : pick_grad<IO, false, true>(p);
+  return inter ? pick_grad<IO, true, false>(p) : pick_grad<IO, false, false>(p);
 }
 
 }  // namespace
 
-const void* rope_paired_kernel(int mode, int dtype, bool inter, const RopePlan& p) {
-  return reinterpret_cast<const void*>(dtype == kDtypeBF16  ? pick_rope_mode<BF16>(mode, inter, p)
-                                       : dtype == kDtypeF32 ? pick_rope_mode<F32>(mode, inter, p)
-                                                            : pick_rope_mode<FP8>(mode, inter, p));
+const void* rope_paired_kernel(int mode, int dtype, bool inter, bool axes, const RopePlan& p) {
+  return reinterpret_cast<const void*>(dtype == kDtypeBF16  ? pick_rope_turn<BF16>(mode, inter, axes, p)
+                                       : dtype == kDtypeF32 ? pick_rope_turn<F32>(mode, inter, axes, p)
+                                                            : pick_rope_turn<FP8>(mode, inter, axes, p));
 }
 
-const void* rope_paired_grad_kernel(int dtype, bool inter, const RopePlan& p) {
-  return reinterpret_cast<const void*>(dtype == kDtypeBF16 ? (inter ? pick_grad<BF16, true>(p) : pick_grad<BF16, false>(p))
-                                                           : (inter ? pick_grad<F32, true>(p) : pick_grad<F32, false>(p)));
+const void* rope_paired_grad_kernel(int dtype, bool inter, bool axes, const RopePlan& p) {
+  return reinterpret_cast<const void*>(dtype == kDtypeBF16 ? pick_grad_turn<BF16>(inter, axes, p)
+                                                           : pick_grad_turn<F32>(inter, axes, p));
 }
 
 }  // namespace qkn

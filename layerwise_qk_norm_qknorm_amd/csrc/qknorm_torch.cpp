@@ -40,11 +40,13 @@ std::string shape_of(const at::Tensor& t) {
 
 // A marshalled call: descriptors, and the tensors that their pointers lead to.
 struct Call {
-  enum Kind { ROPE, GRAD, APPEND, ATTEND } kind;
+  enum Kind { ROPE, GRAD, APPEND, ATTEND, ATTEND_WIDE, GATHER } kind;
   qknorm_operand_t q{}, k{}, v{};
   qknorm_grad_operand_t gq{}, gk{};
   qknorm_rope_t rope{};
-  bool has_q = true, has_rope = false;
+  bool has_q = true, has_rope = false, has_axes = false;
+  qknorm_axes_t axes{};
+  std::string axis;           // axes.axis of a call that is kept
   qknorm_cache_t cache{};
   qknorm_batch_t batch{};
   int64_t T = 0, head_dim = 0, gstride = 0, window = 0;
@@ -57,13 +59,28 @@ struct Call {
 
   int run(void* stream) const {
     const qknorm_rope_t* r = has_rope ? &rope : nullptr;
+    qknorm_axes_t ax = axes;
+    ax.axis = reinterpret_cast<const uint8_t*>(axis.data());
     switch (kind) {
-      case ROPE: return qknorm_headwise_rope(&q, &k, T, dtype, eps, head_dim, gstride, r, stream);
+      case ROPE:
+        if (has_axes) return qknorm_headwise_rope_axes(&q, &k, T, dtype, eps, head_dim, gstride, r, &ax, stream);
+        return qknorm_headwise_rope(&q, &k, T, dtype, eps, head_dim, gstride, r, stream);
       case GRAD:
+        if (has_axes)
+          return qknorm_headwise_rope_axes_backward(&gq, &gk, T, dtype, eps, head_dim, gstride, r, &ax, ws, ws_bytes,
+                                                    stream);
         return qknorm_headwise_rope_backward(&gq, &gk, T, dtype, eps, head_dim, gstride, r, ws, ws_bytes, stream);
       case APPEND:
+        if (has_axes)
+          return qknorm_paged_append_axes(has_q ? &q : nullptr, &k, &v, T, dtype, eps, head_dim, gstride, r, &ax,
+                                          &cache, slots, stream);
         return qknorm_paged_append(has_q ? &q : nullptr, &k, &v, T, dtype, eps, head_dim, gstride, r, &cache, slots,
                                    stream);
+      case GATHER:
+        return qknorm_paged_gather(&cache, head_dim, slots, T, dtype, k.y, k.ld_y, v.y, v.ld_y, stream);
+      case ATTEND_WIDE:
+        return qknorm_paged_attend_wide(&q, T, dtype, &cache, head_dim, &batch, scale, causal, window, ws, ws_bytes,
+                                        stream);
       default:
         return qknorm_paged_attend(&q, T, dtype, &cache, head_dim, &batch, scale, causal, window, ws, ws_bytes,
                                    stream);
@@ -181,7 +198,32 @@ qknorm_operand_t side(Call& c, const at::Tensor& x, const at::Tensor* y, const a
   return o;
 }
 
-void rope_of(Call& c, PyObject* table, PyObject* positions, PyObject* interleaved, const at::Tensor& ref) {
+// The axis of every angle, and the positions [axes, T].
+void axes_of(Call& c, PyObject* axes, const at::Tensor& p, const at::Tensor& ref) {
+  c.has_axes = true;
+  PyObject* bytes = PyBytes_Check(axes) ? (Py_INCREF(axes), axes) : PyBytes_FromObject(axes);
+  if (!bytes) {
+    PyErr_Clear();
+    refuse_type("axes must be bytes or a sequence of small integers, the axis of every angle");
+  }
+  c.axis.assign(PyBytes_AS_STRING(bytes), (size_t)PyBytes_GET_SIZE(bytes));
+  Py_DECREF(bytes);
+  if ((int64_t)c.axis.size() != c.rope.rot_dim / 2)
+    refuse("axes must name the axis of every angle: " + std::to_string(c.rope.rot_dim / 2) + " of them, got " +
+           std::to_string(c.axis.size()));
+  if (p.scalar_type() != at::kLong || p.dim() != 2 || p.size(1) != c.T || (c.T > 1 && p.stride(1) != 1) ||
+      p.size(0) < 1 || p.size(0) > QKNORM_MAX_AXES)
+    refuse("positions must be int64 [axes, " + std::to_string(c.T) + "] with contiguous rows, one to " +
+           std::to_string(QKNORM_MAX_AXES) + " of them, got " + c10::toString(p.scalar_type()) + " " + shape_of(p));
+  on_device(p, ref, "positions");
+  c.axes.n_axes = (int)p.size(0);
+  c.axes.ld_positions = p.size(0) > 1 ? p.stride(0) : 0;
+  c.rope.positions = static_cast<const int64_t*>(p.data_ptr());
+}
+
+// axes: NULL where the call has one axis.
+void rope_of(Call& c, PyObject* table, PyObject* positions, PyObject* interleaved, PyObject* axes,
+             const at::Tensor& ref) {
   const at::Tensor* t = tensor(table, "cos_sin");
   if (!t) return;
   if (t->scalar_type() != at::kFloat || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1))
@@ -193,7 +235,10 @@ void rope_of(Call& c, PyObject* table, PyObject* positions, PyObject* interleave
   c.rope.n_positions = t->size(0);
   c.rope.rot_dim = t->size(1);
   c.rope.ld = t->size(0) > 1 ? t->stride(0) : std::max(t->stride(0), t->size(1));
-  c.rope.positions = vector<int64_t>(p, c.T, at::kLong, ref, "positions");
+  if (axes)
+    axes_of(c, axes, p, ref);
+  else
+    c.rope.positions = vector<int64_t>(p, c.T, at::kLong, ref, "positions");
   c.rope.interleaved = truth(interleaved, "interleaved");
   c.held.push_back(*t);
   c.held.push_back(p);
@@ -208,15 +253,17 @@ void strides_of(const at::Tensor& t, int64_t inner, int64_t (&s)[3]) {
 }
 
 // A cache of [pages, heads, page_size, head_dim] tensors (any strides, a
-// head's row contiguous), or of uint8 codes [.., head_dim / 2] with uint8
-// scales [.., head_dim / 32].
-void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs, const at::Tensor& ref) {
+// head's row contiguous), or of uint8 codes [.., head_dim / 2] (MXFP4) or [..,
+// head_dim] (MXFP8) with uint8 scales [.., head_dim / 32]. rows_type: of a cache of rows.
+void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs, const at::Tensor& ref,
+              at::ScalarType rows_type) {
   const at::Tensor &k = needed(pk, "k_cache"), &v = needed(pv, "v_cache");
   const at::Tensor *ks = tensor(pks, "k_scales"), *vs = tensor(pvs, "v_scales");
   if (!ks != !vs) refuse("k_scales and v_scales go together");
-  const bool four = ks != nullptr;
-  const int64_t last = four ? c.head_dim / 2 : c.head_dim;
-  const at::ScalarType type = four ? at::kByte : ref.scalar_type();
+  const bool codes = ks != nullptr;
+  const bool eight = codes && k.dim() == 4 && k.size(3) == c.head_dim;
+  const int64_t last = codes && !eight ? c.head_dim / 2 : c.head_dim;
+  const at::ScalarType type = codes ? at::kByte : rows_type;
   for (const at::Tensor* t : {&k, &v}) {
     if (t->dim() != 4 || t->size(3) != last || t->scalar_type() != type || (last > 1 && t->stride(3) != 1))
       refuse("k_cache and v_cache must be " + std::string(c10::toString(type)) + " [pages, heads, page_size, " +
@@ -231,7 +278,7 @@ void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs,
   if (k.sizes() != v.sizes() || !std::equal(s, s + 3, sv))
     refuse("k_cache and v_cache must have the same shape and strides");
   qknorm_cache_t& o = c.cache;
-  o.format = four ? QKNORM_CACHE_MXFP4 : QKNORM_CACHE_ROWS;
+  o.format = eight ? QKNORM_CACHE_MXFP8 : codes ? QKNORM_CACHE_MXFP4 : QKNORM_CACHE_ROWS;
   o.k = k.data_ptr();
   o.v = v.data_ptr();
   o.n_pages = k.size(0);
@@ -240,7 +287,7 @@ void cache_of(Call& c, PyObject* pk, PyObject* pv, PyObject* pks, PyObject* pvs,
   o.page_stride = s[0];
   o.head_stride = s[1];
   o.token_stride = s[2];
-  if (!four) return;
+  if (!codes) return;
   const int64_t blocks = c.head_dim / 32;
   for (const at::Tensor* t : {ks, vs}) {
     if (t->dim() != 4 || t->size(0) != o.n_pages || t->size(1) != o.heads || t->size(2) != o.page_size ||
@@ -278,7 +325,7 @@ void workspace_of(Call& c, PyObject* given, size_t need, const at::Tensor& ref) 
 }
 
 // ---------------------------------------------------------------------- calls
-void make_rope(Call& c, PyObject* const* a) {
+void make_rope_of(Call& c, PyObject* const* a, PyObject* axes) {
   const at::Tensor &q = needed(a[0], "q"), &k = needed(a[1], "k");
   c.kind = Call::ROPE;
   c.T = same_tokens(q, k);
@@ -288,9 +335,11 @@ void make_rope(Call& c, PyObject* const* a) {
   const at::Tensor *oq = tensor(a[10], "out_q"), *ok = tensor(a[11], "out_k");
   c.q = side(c, q, oq ? oq : &q, &needed(a[2], "gamma_q"), "q");
   c.k = side(c, k, ok ? ok : &k, &needed(a[3], "gamma_k"), "k");
-  rope_of(c, a[6], a[7], a[8], q);
+  rope_of(c, a[6], a[7], a[8], axes, q);
   c.dtype = dtype_code(q);
 }
+void make_rope(Call& c, PyObject* const* a) { make_rope_of(c, a, nullptr); }
+void make_rope_axes(Call& c, PyObject* const* a) { make_rope_of(c, a, a[12]); }
 
 qknorm_grad_operand_t grad_side(Call& c, const at::Tensor& x, PyObject* dy, PyObject* gamma, PyObject* dx,
                                 PyObject* dgamma, const char* name) {
@@ -318,7 +367,7 @@ qknorm_grad_operand_t grad_side(Call& c, const at::Tensor& x, PyObject* dy, PyOb
   return o;
 }
 
-void make_grad(Call& c, PyObject* const* a) {
+void make_grad_of(Call& c, PyObject* const* a, PyObject* axes) {
   const at::Tensor &q = needed(a[2], "q"), &k = needed(a[3], "k");
   c.kind = Call::GRAD;
   c.T = same_tokens(q, k);
@@ -327,15 +376,17 @@ void make_grad(Call& c, PyObject* const* a) {
   c.gstride = integer(a[11], "gamma_head_stride");
   c.gq = grad_side(c, q, a[0], a[4], a[12], a[14], "q");
   c.gk = grad_side(c, k, a[1], a[5], a[13], a[15], "k");
-  rope_of(c, a[8], a[9], a[10], q);
+  rope_of(c, a[8], a[9], a[10], axes, q);
   c.dtype = dtype_code(q);
   size_t need = 0;
   if (c.gq.dgamma || c.gk.dgamma)
     need = qknorm_headwise_rope_backward_workspace(c.gq.h, c.gk.h, c.T, c.dtype, c.head_dim, c.gstride);
   workspace_of(c, a[16], need, q);
 }
+void make_grad(Call& c, PyObject* const* a) { make_grad_of(c, a, nullptr); }
+void make_grad_axes(Call& c, PyObject* const* a) { make_grad_of(c, a, a[17]); }
 
-void make_append(Call& c, PyObject* const* a) {
+void make_append_of(Call& c, PyObject* const* a, PyObject* axes) {
   const at::Tensor* q = tensor(a[0], "q");
   const at::Tensor &k = needed(a[1], "k"), &v = needed(a[2], "v");
   c.kind = Call::APPEND;
@@ -351,23 +402,49 @@ void make_append(Call& c, PyObject* const* a) {
   }
   c.k = side(c, k, tensor(a[17], "out_k"), tensor(a[4], "gamma_k"), "k");
   c.v = side(c, v, tensor(a[18], "out_v"), nullptr, "v");
-  cache_of(c, a[9], a[10], a[12], a[13], k);
-  rope_of(c, a[7], a[8], a[14], k);
+  cache_of(c, a[9], a[10], a[12], a[13], k, k.scalar_type());
+  rope_of(c, a[7], a[8], a[14], axes, k);
   const at::Tensor& s = needed(a[11], "slots");
   c.slots = vector<int64_t>(s, c.T, at::kLong, k, "slots");
   c.held.push_back(s);
   c.dtype = dtype_code(k);
 }
+void make_append(Call& c, PyObject* const* a) { make_append_of(c, a, nullptr); }
+void make_append_axes(Call& c, PyObject* const* a) { make_append_of(c, a, a[19]); }
 
-void make_attend(Call& c, PyObject* const* a) {
+void make_gather(Call& c, PyObject* const* a) {
+  const at::Tensor &slots = needed(a[2], "slots");
+  const at::Tensor *ok = tensor(a[6], "out_k"), *ov = tensor(a[7], "out_v");
+  const at::Tensor* ref = ok ? ok : ov;
+  if (!ref) refuse("out_k or out_v is required");
+  c.kind = Call::GATHER;
+  c.head_dim = integer(a[3], "head_dim");
+  rows(*ref, "out");                                  // the rows are on a GPU
+  c.T = ref->size(0);
+  cache_of(c, a[0], a[1], a[4], a[5], *ref, ref->scalar_type());
+  for (const at::Tensor* t : {ok, ov}) {
+    if (!t) continue;
+    qknorm_operand_t& o = t == ok ? c.k : c.v;
+    if (t->dim() != 2 || t->size(1) != c.cache.heads * c.head_dim)
+      refuse("out_k and out_v must be [T, " + std::to_string(c.cache.heads * c.head_dim) + "], got " + shape_of(*t));
+    o.ld_y = like(*t, *ref, "out_k and out_v");
+    o.y = t->data_ptr();
+    c.held.push_back(*t);
+  }
+  c.slots = vector<int64_t>(slots, c.T, at::kLong, *ref, "slots");
+  c.held.push_back(slots);
+  c.dtype = dtype_code(*ref);
+}
+
+void make_attend_of(Call& c, PyObject* const* a, bool wide) {
   const at::Tensor &q = needed(a[0], "q"), &table = needed(a[5], "block_table"), &lens = needed(a[6], "seq_lens");
   const at::Tensor* cu = tensor(a[8], "cu_q");
-  c.kind = Call::ATTEND;
-  if (a[3] == Py_None || a[4] == Py_None) refuse("k_scales and v_scales are required: the cache is MXFP4");
+  c.kind = wide ? Call::ATTEND_WIDE : Call::ATTEND;
+  if (!wide && (a[3] == Py_None || a[4] == Py_None)) refuse("k_scales and v_scales are required: the cache is MXFP4");
   c.head_dim = integer(a[7], "head_dim");
   c.q = side(c, q, &needed(a[14], "out"), nullptr, "q");
   c.T = q.size(0);
-  cache_of(c, a[1], a[2], a[3], a[4], q);
+  cache_of(c, a[1], a[2], a[3], a[4], q, at::kBFloat16);
   if (table.dim() != 2 || table.scalar_type() != at::kInt || (table.size(1) > 1 && table.stride(1) != 1))
     refuse("block_table must be int32 [B, pages] with contiguous rows");
   on_device(table, q, "block_table");
@@ -393,9 +470,12 @@ void make_attend(Call& c, PyObject* const* a) {
   c.dtype = dtype_code(q);
   size_t need = 0;
   if (c.head_dim > 0 && c.cache.heads > 0)
-    need = qknorm_paged_attend_workspace(c.T, c.q.h / c.head_dim, c.cache.heads, c.head_dim, b.B, b.max_q, b.max_len);
+    need = (wide ? qknorm_paged_attend_wide_workspace : qknorm_paged_attend_workspace)(
+        c.T, c.q.h / c.head_dim, c.cache.heads, c.head_dim, b.B, b.max_q, b.max_len);
   workspace_of(c, a[15], need, q);
 }
+void make_attend(Call& c, PyObject* const* a) { make_attend_of(c, a, false); }
+void make_attend_wide(Call& c, PyObject* const* a) { make_attend_of(c, a, true); }
 
 // --------------------------------------------------------------------- module
 constexpr const char* kCapsule = "_qknorm_torch.call";
@@ -436,6 +516,11 @@ PyMethodDef methods[] = {
     {"rope_backward", (PyCFunction)(void*)entry<make_grad, 17>, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void*)entry<make_append, 19>, METH_FASTCALL, nullptr},
     {"attend", (PyCFunction)(void*)entry<make_attend, 16>, METH_FASTCALL, nullptr},
+    {"rope_axes", (PyCFunction)(void*)entry<make_rope_axes, 13>, METH_FASTCALL, nullptr},
+    {"rope_axes_backward", (PyCFunction)(void*)entry<make_grad_axes, 18>, METH_FASTCALL, nullptr},
+    {"append_axes", (PyCFunction)(void*)entry<make_append_axes, 20>, METH_FASTCALL, nullptr},
+    {"attend_wide", (PyCFunction)(void*)entry<make_attend_wide, 16>, METH_FASTCALL, nullptr},
+    {"gather", (PyCFunction)(void*)entry<make_gather, 8>, METH_FASTCALL, nullptr},
     {"launch", (PyCFunction)(void*)launch, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qknorm_torch", nullptr, -1, methods};

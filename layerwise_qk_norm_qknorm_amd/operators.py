@@ -1,7 +1,8 @@
 """Binding of the operators around headwise QK-Norm: the norm with the
-position rotation in the same pass, its gradients, appending to a paged key /
-value cache and attention over the 4-bit cache (argument marshalling only, in
-the C++ module ``_qknorm_torch``; the C names are kept).
+position rotation in the same pass (one position a token, or one for each of
+several axes), its gradients, appending to a paged key / value cache, reading it
+back and attention over it (argument marshalling only, in the C++ module
+``_qknorm_torch``; the C names are kept).
 
 The calls run on torch's current stream of the tensors' device, whichever
 device is current, or on ``stream``. What a call allocates itself (outputs or
@@ -51,6 +52,24 @@ def rope_table(n_positions, rot_dim, base=10000.0, inv_freq=None, device="cuda")
             raise ValueError(f"inv_freq must have shape ({rot_dim // 2},)")
     angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * inv_freq[None, :]
     return torch.cat((angle.cos(), angle.sin()), 1).to(torch.float32)
+
+
+def rope_axes(sections, spread=False):
+    """The axis of every angle, as the calls with several axes take it (bytes): sections[a]
+    angles of axis a one after the other, (16, 24, 24) for time, height and width of 64 angles;
+    spread: dealt to the axes in turn, while each has some left."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0:
+        raise ValueError(f"sections must be one to four counts of angles, got {tuple(sections)}")
+    if not spread:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    out = bytearray()
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                out.append(a)
+    return bytes(out)
 
 
 class _OperatorCall(PreparedCall):
@@ -154,6 +173,24 @@ def prepare_headwise_rope(q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positi
                      (q if out_q is None else out_q, k if out_k is None else out_k))
 
 
+def qknorm_headwise_rope_axes(q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, axes, interleaved=False,
+                              gamma_head_stride=0, out_q=None, out_k=None, stream=None):
+    """``qknorm_headwise_rope`` with positions on several axes (images and video: time, height,
+    width): positions int64 [n_axes, T], at most four, and ``axes`` the axis of each of the
+    rot_dim / 2 angles, as bytes (``rope_axes``) or a sequence."""
+    _run("rope_axes", (q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, interleaved, gamma_head_stride,
+                       out_q, out_k, axes), q, stream)
+    return (q if out_q is None else out_q), (k if out_k is None else out_k)
+
+
+def prepare_headwise_rope_axes(q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, axes, interleaved=False,
+                               gamma_head_stride=0, out_q=None, out_k=None):
+    """qknorm_headwise_rope_axes with its arguments checked and marshalled once (PreparedCall)."""
+    return _prepared("rope_axes", (q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, interleaved,
+                                   gamma_head_stride, out_q, out_k, axes), q,
+                     (q if out_q is None else out_q, k if out_k is None else out_k))
+
+
 # ------------------------------------------------------------------------ gradients
 def _new_gradient(gamma, x, head_dim, stride):
     """dgamma for gamma: elements that no head has, and all of them for no tokens, are 0."""
@@ -217,6 +254,33 @@ def prepare_headwise_rope_backward(dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head
                      (m for m, g in zip(made, given) if g is None))
 
 
+def qknorm_headwise_rope_axes_backward(dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, axes,
+                                       interleaved=False, gamma_head_stride=0, dx_q=None, dx_k=None, dgamma_q=None,
+                                       dgamma_k=None, need_dgamma=True, workspace=None, stream=None):
+    """Gradients of ``qknorm_headwise_rope_axes``: as ``qknorm_headwise_rope_backward``, with its
+    positions and axes."""
+    dx_q, dx_k, dgamma_q, dgamma_k, workspace = _gradient_outputs(
+        q, k, gamma_q, gamma_k, head_dim, gamma_head_stride, dx_q, dx_k, dgamma_q, dgamma_k, need_dgamma, workspace,
+        stream)
+    _run("rope_axes_backward", (dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, interleaved,
+                                gamma_head_stride, dx_q, dx_k, dgamma_q, dgamma_k, workspace, axes), q, stream)
+    return dx_q, dx_k, dgamma_q, dgamma_k
+
+
+def prepare_headwise_rope_axes_backward(dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, axes,
+                                        interleaved=False, gamma_head_stride=0, dx_q=None, dx_k=None, dgamma_q=None,
+                                        dgamma_k=None, need_dgamma=True, workspace=None):
+    """qknorm_headwise_rope_axes_backward with its arguments checked and marshalled once
+    (PreparedCall). It keeps its workspace: calls of one object must not run at the same time on
+    two streams."""
+    given = (dx_q, dx_k, dgamma_q, dgamma_k, workspace)
+    made = _gradient_outputs(q, k, gamma_q, gamma_k, head_dim, gamma_head_stride, *given[:4], need_dgamma, workspace,
+                             _current(q))
+    return _prepared("rope_axes_backward", (dy_q, dy_k, q, k, gamma_q, gamma_k, eps, head_dim, cos_sin, positions,
+                                            interleaved, gamma_head_stride, *made, axes), q, made[:4],
+                     (m for m, g in zip(made, given) if g is None))
+
+
 # ---------------------------------------------------------------------- paged cache
 def qknorm_paged_append(q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, k_cache, v_cache, slots,
                         k_scales=None, v_scales=None, interleaved=False, gamma_head_stride=0, out_q=None, out_k=None,
@@ -227,7 +291,7 @@ def qknorm_paged_append(q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, posit
 
     gamma_q / gamma_k None: that side is rotated only. k_cache, v_cache: the row type
     [pages, heads, page_size, head_dim], or with k_scales and v_scales (uint8 [.., head_dim / 32])
-    MXFP4 codes, uint8 [.., head_dim / 2]. slots: int64 [T], page * page_size + place; a token
+    codes: MXFP4, uint8 [.., head_dim / 2], or MXFP8, uint8 [.., head_dim]. slots: int64 [T], page * page_size + place; a token
     with a negative slot is passed over (nothing of its row is written), and no two may have
     the same. out_k / out_v, if given, receive as rows what the cache now holds. Returns out_q."""
     _run("append", (q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, k_cache, v_cache, slots, k_scales,
@@ -244,7 +308,62 @@ def prepare_paged_append(q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, posi
                      q if out_q is None else out_q)
 
 
-def _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace, stream):
+def qknorm_paged_append_axes(q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, axes, k_cache, v_cache,
+                             slots, k_scales=None, v_scales=None, interleaved=False, gamma_head_stride=0, out_q=None,
+                             out_k=None, out_v=None, stream=None):
+    """``qknorm_paged_append`` with positions on several axes (``qknorm_headwise_rope_axes``)."""
+    _run("append_axes", (q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, k_cache, v_cache, slots,
+                         k_scales, v_scales, interleaved, gamma_head_stride, out_q, out_k, out_v, axes), k, stream)
+    return q if out_q is None else out_q
+
+
+def prepare_paged_append_axes(q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, axes, k_cache, v_cache,
+                              slots, k_scales=None, v_scales=None, interleaved=False, gamma_head_stride=0, out_q=None,
+                              out_k=None, out_v=None):
+    """qknorm_paged_append_axes with its arguments checked and marshalled once (PreparedCall)."""
+    return _prepared("append_axes", (q, k, v, gamma_q, gamma_k, eps, head_dim, cos_sin, positions, k_cache, v_cache,
+                                     slots, k_scales, v_scales, interleaved, gamma_head_stride, out_q, out_k, out_v,
+                                     axes), k, q if out_q is None else out_q)
+
+
+def _gather_rows(k_cache, v_cache, slots, head_dim, k_scales, out_k, out_v, dtype, stream):
+    """The rows that were not passed: both, where neither was, in memory of `stream`. Rows that no
+    slot fills are 0."""
+    if out_k is not None or out_v is not None:
+        return out_k, out_v
+    if not (isinstance(slots, torch.Tensor) and slots.dim() == 1 and k_cache.dim() == 4):
+        raise ValueError("slots must be a vector, the caches [pages, heads, page_size, ..]")
+    if dtype is None:
+        dtype = k_cache.dtype if k_scales is None else torch.bfloat16
+    with _at(stream, k_cache.device):
+        return tuple(torch.zeros((slots.shape[0], k_cache.shape[1] * head_dim), dtype=dtype, device=k_cache.device)
+                     for _ in range(2))
+
+
+def qknorm_paged_gather(k_cache, v_cache, slots, head_dim, k_scales=None, v_scales=None, out_k=None, out_v=None,
+                        dtype=None, stream=None):
+    """Reads a paged cache back: row t of out_k and out_v [T, heads * head_dim] gets what slot
+    slots[t] holds (``qknorm_paged_append``'s caches and slots, its inverse). A negative slot
+    leaves its row as it was.
+
+    out_k, out_v: the one that is passed alone is the only one read; both are allocated (zeroed)
+    where neither is passed, of ``dtype``: the cache's own for rows, by default bfloat16 for
+    codes, or float32. Returns (out_k, out_v)."""
+    out_k, out_v = _gather_rows(k_cache, v_cache, slots, head_dim, k_scales, out_k, out_v, dtype, stream)
+    _run("gather", (k_cache, v_cache, slots, head_dim, k_scales, v_scales, out_k, out_v),
+         out_v if out_k is None else out_k, stream)
+    return out_k, out_v
+
+
+def prepare_paged_gather(k_cache, v_cache, slots, head_dim, k_scales=None, v_scales=None, out_k=None, out_v=None,
+                         dtype=None):
+    """qknorm_paged_gather with its arguments checked and marshalled once (PreparedCall)."""
+    made = _gather_rows(k_cache, v_cache, slots, head_dim, k_scales, out_k, out_v, dtype, _current(k_cache))
+    return _prepared("gather", (k_cache, v_cache, slots, head_dim, k_scales, v_scales, *made),
+                     made[1] if made[0] is None else made[0], made, made if out_k is None and out_v is None else ())
+
+
+def _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace, stream, wide=False):
     """The output and the workspace that were not passed, in memory of `stream`."""
     if out is None or (stream is not None and workspace is None):
         with _at(stream, q.device):
@@ -252,7 +371,8 @@ def _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out,
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             if stream is not None and workspace is None and head_dim > 0 and k_cache.dim() == 4:
                 capacity = block_table.shape[1] * k_cache.shape[2]
-                need = load_library().qknorm_paged_attend_workspace(
+                lib = load_library()
+                need = (lib.qknorm_paged_attend_wide_workspace if wide else lib.qknorm_paged_attend_workspace)(
                     q.shape[0], q.shape[1] // head_dim, k_cache.shape[1], head_dim, block_table.shape[0],
                     1 if cu_q is None else max(q.shape[0], 1) if max_q is None else max_q,
                     capacity if max_len is None else min(max_len, capacity))
@@ -289,4 +409,31 @@ def prepare_paged_attend(q, k_cache, v_cache, k_scales, v_scales, block_table, s
                           _current(q))
     return _prepared("attend", (q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, head_dim, cu_q, scale,
                                 causal, window, max_q, max_len, *made), q, made[0],
+                     (m for m, g in zip(made, given) if g is None))
+
+
+def qknorm_paged_attend_wide(q, k_cache, v_cache, block_table, seq_lens, head_dim, k_scales=None, v_scales=None,
+                             cu_q=None, scale=None, causal=True, window=0, max_q=None, max_len=None, out=None,
+                             workspace=None, stream=None):
+    """Attention of bf16 query rows q [T, heads * head_dim] over a paged cache of bf16 rows, or with
+    k_scales and v_scales of MXFP8 codes (``qknorm_paged_append``'s layouts): prompts, chunks of
+    new tokens behind what the cache holds, and single tokens. Pages hold at least 16 tokens.
+
+    workspace: uint8, at least ``qknorm_paged_attend_wide_workspace`` bytes; allocated if None.
+    The other arguments are those of ``qknorm_paged_attend``. Returns ``out``."""
+    out, workspace = _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace, stream, True)
+    _run("attend_wide", (q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, head_dim, cu_q, scale, causal,
+                         window, max_q, max_len, out, workspace), q, stream)
+    return out
+
+
+def prepare_paged_attend_wide(q, k_cache, v_cache, block_table, seq_lens, head_dim, k_scales=None, v_scales=None,
+                              cu_q=None, scale=None, causal=True, window=0, max_q=None, max_len=None, out=None,
+                              workspace=None):
+    """qknorm_paged_attend_wide with its arguments checked and marshalled once (PreparedCall): for
+    decode loops, as ``prepare_paged_attend``."""
+    given = (out, workspace)
+    made = _attend_memory(q, k_cache, block_table, head_dim, cu_q, max_q, max_len, out, workspace, _current(q), True)
+    return _prepared("attend_wide", (q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, head_dim, cu_q,
+                                     scale, causal, window, max_q, max_len, *made), q, made[0],
                      (m for m, g in zip(made, given) if g is None))
