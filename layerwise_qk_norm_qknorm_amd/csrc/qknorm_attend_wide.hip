@@ -7,8 +7,7 @@
 // when m grows. MXFP8 codes are widened to bf16 with their scale applied,
 // exactly (four significant bits times a power of two), so both products run on
 // bf16 MFMA tiles with nothing lost on the K and V side. Probabilities are
-// rounded to bf16 (at most half a step, 2^-9 of the largest, averaged over the
-// tokens); scores, m, l and the accumulator are float32, and l sums the rounded
+// rounded to bf16 (at most half a step, 2^-8 relative, averaged over the tokens); scores, m, l and the accumulator are float32, and l sums the rounded
 // probabilities.
 //
 // Scores are formed transposed (tokens x rows), so that a lane holds one row's

@@ -422,9 +422,10 @@ void make_gather(Call& c, PyObject* const* a) {
   rows(*ref, "out");                                  // the rows are on a GPU
   c.T = ref->size(0);
   cache_of(c, a[0], a[1], a[4], a[5], *ref, ref->scalar_type());
-  for (const at::Tensor* t : {ok, ov}) {
+  for (int i = 0; i < 2; ++i) {
+    const at::Tensor* t = i ? ov : ok;
     if (!t) continue;
-    qknorm_operand_t& o = t == ok ? c.k : c.v;
+    qknorm_operand_t& o = i ? c.v : c.k;
     if (t->dim() != 2 || t->size(1) != c.cache.heads * c.head_dim)
       refuse("out_k and out_v must be [T, " + std::to_string(c.cache.heads * c.head_dim) + "], got " + shape_of(*t));
     o.ld_y = like(*t, *ref, "out_k and out_v");

@@ -138,3 +138,46 @@ def attend(q, K, V, n_q, scale, causal, window):
                 out[i, h] = p @ V[lo:hi, kh]
                 mag[i, h] = p @ np.abs(V[lo:hi, kh])
     return out, mag, some
+
+
+# E4M3 (OCP 8-bit floating point): magnitudes by code, the sign is bit 7; 127 is NaN.
+E4M3 = np.array([m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10) for e in range(16) for m in range(8)][:127])
+
+
+def mxfp8_quantize(x):
+    """x [..., d] (d a multiple of 32) -> (codes uint8 [..., d], scale bytes uint8 [..., d/32],
+    values float64 [..., d]). Scale 2^E with E = floor(log2(largest magnitude)) - 8 held to
+    [-100, 119]; the nearest E4M3 value, ties to the even code, at most 448; a block with an
+    infinity or NaN: codes 0, scale byte 255, values NaN."""
+    x = np.asarray(x, np.float64)
+    b = x.reshape(*x.shape[:-1], -1, 32)
+    ok = np.isfinite(b).all(-1)
+    safe = np.where(ok[..., None], b, 0.0)
+    amax = np.abs(safe).max(-1)
+    _, e = np.frexp(amax)                       # amax = m 2^e, m in [1/2, 1)
+    E = np.where(amax > 0, np.clip(e - 9, -100, 119), -100)
+    a = np.minimum(np.ldexp(np.abs(safe), -E[..., None]), 448.0)
+    hi = np.searchsorted(E4M3, a)               # the first value not below
+    lo = np.maximum(hi - 1, 0)
+    up, down = E4M3[hi] - a, a - E4M3[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    value = np.ldexp(E4M3[code], E[..., None]) * np.where(np.signbit(safe), -1.0, 1.0)
+    code = (code + 128 * np.signbit(safe)).reshape(x.shape).astype(np.uint8)
+    scale = np.where(ok, E + 127, 255).astype(np.uint8)
+    return code, scale, np.where(ok[..., None], value, np.nan).reshape(x.shape)
+
+
+def mxfp8_values(codes, scales):
+    """float64 values of codes [..., d] with scale bytes [..., d/32]; bytes above 246, and the codes
+    127 and 255: NaN."""
+    x = np.append(E4M3, np.nan)[codes & 127] * np.where(codes & 128, -1.0, 1.0)
+    s = np.where(scales <= 246, np.ldexp(1.0, scales.astype(np.int64) - 127), np.nan)
+    return x * np.repeat(s, 32, axis=-1)
+
+
+def axis_angles(table, positions, axis, rot):
+    """cos and sin [T, rot/2] at positions [axes, T], angle i at its axis[i]'s."""
+    rows = [angles(table, p, rot) for p in positions]
+    i = np.arange(rot // 2)
+    axis = np.asarray(list(axis), dtype=np.int64)
+    return tuple(np.stack([r[j] for r in rows])[axis, :, i].T for j in (0, 1))
