@@ -527,23 +527,73 @@ __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) qknorm_attend_f
 }
 
 // ----------------------------------------------------------------- many rows
+// A block's sequence, key head, tile of rows (kBlock) and split of the cache. Blocks
+// take different times (a sequence's length, a row's place in it) and are more than
+// the chip holds at once, so the longest go first: up to 64 sequences by their
+// cached tokens, each one's last rows first, and blocks for rows that a sequence
+// does not have come last of all. 4 x 531 .. 1024 rows on 4215 .. 8192 tokens, 40
+// over 8 heads of 128: in the order of the sequences 680 us, so ordered 540.
+// Consecutive blocks take the key heads in turn: where they divide by 8, a head's
+// blocks run on one XCD, whose L2 then holds its cache.
+struct Work {
+  int b, hk, tile, split;
+};
+__device__ __forceinline__ Work work_of(const AttendArgs& a, int block_rows) {
+  Work w;
+  if (a.B > 64) {
+    const uint32_t rest = over(blockIdx.x, a.by_pairs);
+    const uint32_t pair = blockIdx.x - rest * a.by_pairs.d;
+    const uint32_t rev = over(rest, a.by_splits);
+    w.split = rest - rev * a.by_splits.d;
+    w.tile = a.row_tiles - 1 - (int)rev;
+    w.b = over(pair, a.by_heads);
+    w.hk = pair - w.b * a.heads_k;
+    return w;
+  }
+  const uint32_t rest = over(blockIdx.x, a.by_heads);
+  w.hk = blockIdx.x - rest * a.by_heads.d;
+  const uint32_t unit = over(rest, a.by_splits);
+  w.split = rest - unit * a.by_splits.d;
+  // lane b: a sequence's tiles, and those of the ones before it
+  const int lane = threadIdx.x & 63;
+  int tiles = 0, len = -1;
+  if (lane < a.B) {
+    const Sequence s = sequence(a, lane);
+    len = s.len;
+    tiles = min((s.nq * a.group + block_rows - 1) / block_rows, a.row_tiles);
+  }
+  int before = 0;
+  for (int x = 0; x < a.B; ++x) {
+    const int l = __builtin_amdgcn_readlane(len, x), n = __builtin_amdgcn_readlane(tiles, x);
+    if (l > len || (l == len && x < lane)) before += n;
+  }
+  const uint64_t mine = __builtin_amdgcn_ballot_w64((int)unit >= before && (int)unit < before + tiles);
+  if (mine == 0) {
+    w.b = -1;
+    return w;
+  }
+  w.b = __builtin_ctzll(mine);
+  w.tile = __builtin_amdgcn_readlane(tiles, w.b) - 1 - ((int)unit - __builtin_amdgcn_readlane(before, w.b));
+  return w;
+}
+
 // NT tiles of 32 rows a wave. K and V tiles of kTok tokens in LDS, two of each:
 // one is read while the next one, loaded into registers behind the products,
 // waits to be written.
-template <class F, int D, int NT>
-__global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) qknorm_attend_many(const AttendArgs a) {
+template <class F, int D, int NT, int NW>
+__global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qknorm_attend_many(const AttendArgs a) {
   constexpr int kTok = 64;
   constexpr int MB = D / 32;                 // 32-channel blocks of the output
   constexpr int KS = D / 16;                 // steps of the first product
   constexpr int kPer = D / F::kVW;           // lanes across a token
   constexpr int kAt = 64 / kPer;             // tokens of one wave's load
-  constexpr int PL = kTok / (kWaves * kAt);  // loads a thread makes of K, and of V
-  constexpr int LDK = D * 2 + 16, LDV = D * 2 + 32;   // bytes of a row: neighbouring rows in distinct banks
-  constexpr int kBlock = 32 * NT * kWaves;   // rows of a block
+  constexpr int PL = kTok / (NW * kAt);  // loads a thread makes of K, and of V
+  constexpr int LDK = D * 2 + 16, LDV = D * 2 + 64;   // bytes of a row: no two of those read together share a bank
+  constexpr int kBlock = 32 * NT * NW;   // rows of a block
   constexpr int kTileK = kTok * LDK, kTileV = kTok * LDV;
   constexpr int LDO = D + 4;                 // padded row of the results on their way out
-  __shared__ __align__(16) char lds[2 * (kTileK + kTileV)];
-  static_assert(kWaves * 32 * LDO * 4 <= (int)sizeof(lds), "the results fit the tiles' place");
+  constexpr int kTiles = 2 * (kTileK + kTileV), kResults = NW * 32 * LDO * 4;
+  __shared__ __align__(16) char lds[kTiles > kResults ? kTiles : kResults];
   char* const kbuf = lds;
   char* const vbuf = lds + 2 * kTileK;
   __shared__ int unusual;                    // some tile at an edge held infinities or NaN
@@ -551,13 +601,9 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) qknorm_att
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 31, g = lane >> 5;
-  const uint32_t rest = over(blockIdx.x, a.by_pairs);
-  const uint32_t pair = blockIdx.x - rest * a.by_pairs.d;
-  const uint32_t tile_rev = over(rest, a.by_splits);
-  const int split = rest - tile_rev * a.by_splits.d;
-  const int grid_tile = a.row_tiles - 1 - (int)tile_rev;   // long rows first
-  const int b = over(pair, a.by_heads);
-  const int hk = pair - b * a.heads_k;
+  const Work at_work = work_of(a, kBlock);
+  const int split = at_work.split, grid_tile = at_work.tile, b = at_work.b, hk = at_work.hk;
+  if (b < 0) return;
 
   const Sequence seq = sequence(a, b);
   const int32_t* table = a.table + b * a.ld_table;
@@ -621,14 +667,25 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) qknorm_att
       const int end = min(begin + a.chunk, sp.hi);
       const int last16 = (end - 1) & ~15;
       Raw K[PL], V[PL];
-      bool lost[PL];
-      // this wave's share of a tile: tokens (x * kWaves + wave) * kAt and on
+      uint32_t lost = 0;               // bits of the loads whose page does not exist
+      // page ids of the next 64 groups of 16 tokens, a lane's each: one load for 16
+      // tiles, ahead of its use (a scalar lookup would hold up the tile's loads)
+      const auto pages_from = [&](int tok) { return table[min(tok + 16 * lane, last16) >> a.log2_page]; };
+      int ids = pages_from(begin), ids_from = begin, ids_next = pages_from(begin + 1024);
+      // this wave's share of a tile: tokens (x * NW + wave) * kAt and on
       const auto load = [&](int tok) {
+        if (tok >= ids_from + 1024) {
+          ids_from += 1024;
+          ids = ids_next;
+          ids_next = pages_from(ids_from + 1024);
+        }
+        lost = 0;
 #pragma unroll
         for (int x = 0; x < PL; ++x) {
-          const int t = tok + (x * kWaves + wave) * kAt;
-          const Group at = group_at<D>(a, page_of(a, table, t, last16), t, last16);
-          lost[x] = at.lost;
+          const int t = tok + (x * NW + wave) * kAt;
+          const int id = __builtin_amdgcn_readlane(ids, (t - ids_from) >> 4);
+          const Group at = group_at<D>(a, id, t, last16);
+          lost |= (uint32_t)at.lost << x;
           const u32x4_t w = load_at<u32x4_t>(ksrc.rows + at.rows, off);
           K[x].w[0] = w.x, K[x].w[1] = w.y, K[x].w[2] = w.z, K[x].w[3] = w.w;
           const u32x4_t v = load_at<u32x4_t>(vsrc.rows + at.rows, off);
@@ -639,33 +696,46 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) qknorm_att
           }
         }
       };
+      const int put_k = lane / kPer * LDK + lane % kPer * (F::kVW * 2), put_v = lane / kPer * LDV + lane % kPer * (F::kVW * 2);
       const auto store = [&](int tok, int buf) {
         const bool edge = tok < block_lo || tok + kTok > min(block_hi, end);
+        uint32_t top = 0;
+        if constexpr (F::kCodes) {
 #pragma unroll
-        for (int x = 0; x < PL; ++x) {
-          const int row = (x * kWaves + wave) * kAt + lane / kPer;
-          Piece16<F> p;
-          p.widen(K[x]);
-          if (lost[x] || (F::kCodes && __builtin_amdgcn_ballot_w64(K[x].scale > kTopScale8) != 0)) {
-            keep_branch();
-            if (lost[x] || K[x].scale > kTopScale8) p.fill(kNaNs);
-          }
-          p.to_lds(kbuf + buf * kTileK + row * LDK + (lane % kPer) * (F::kVW * 2));
-          p.widen(V[x]);
-          if (F::kCodes && __builtin_amdgcn_ballot_w64(V[x].scale > kTopScale8) != 0) {
-            keep_branch();
-            if (V[x].scale > kTopScale8) p.fill(kNaNs);
-          }
-          if (edge || lost[x]) {
-            keep_branch();
+          for (int x = 0; x < PL; ++x) top = max(top, max(K[x].scale, V[x].scale));
+        }
+        char* const kd = kbuf + buf * kTileK + put_k;
+        char* const vd = vbuf + buf * kTileV + put_v;
+        if (edge || lost != 0 || (F::kCodes && __builtin_amdgcn_ballot_w64(top > kTopScale8) != 0)) {
+          keep_branch();
+#pragma unroll
+          for (int x = 0; x < PL; ++x) {
+            const int row = (x * NW + wave) * kAt;
+            const bool gone = lost >> x & 1;
+            Piece16<F> p;
+            p.widen(K[x]);
+            if (gone || (F::kCodes && K[x].scale > kTopScale8)) p.fill(kNaNs);
+            p.to_lds(kd + row * LDK);
+            p.widen(V[x]);
+            if (F::kCodes && V[x].scale > kTopScale8) p.fill(kNaNs);
             // behind the end of the sequence lies whatever the page held
-            if (lost[x] || tok + row >= seq.len) p.fill(0);
-            if (__builtin_amdgcn_ballot_w64(p.unusual()) != 0) {
+            if (gone || tok + row + lane / kPer >= seq.len) p.fill(0);
+            if (edge && __builtin_amdgcn_ballot_w64(p.unusual()) != 0) {
               p.drop_unusual();
               if (lane == 0) unusual = 1;
             }
+            p.to_lds(vd + row * LDV);
           }
-          p.to_lds(vbuf + buf * kTileV + row * LDV + (lane % kPer) * (F::kVW * 2));
+        } else {
+#pragma unroll
+          for (int x = 0; x < PL; ++x) {
+            const int row = (x * NW + wave) * kAt;
+            Piece16<F> p;
+            p.widen(K[x]);
+            p.to_lds(kd + row * LDK);
+            p.widen(V[x]);
+            p.to_lds(vd + row * LDV);
+          }
         }
       };
       int tok = begin, cur = 0;
@@ -678,75 +748,90 @@ __global__ void __launch_bounds__(64 * kWaves, NT * D <= 128 ? 2 : 1) qknorm_att
         if (more) load(tok + kTok);
         if (tok < any_hi && tok + kTok > any_lo) {     // some row of this wave sees something
           const bool edge = tok < lo_all || tok + kTok > min(hi_all, end);
+          // scores of both 32-token halves, transposed: lane (m, g) gets tokens
+          // 32 tb + 8 (i / 4) + 4g + i % 4 of row m
+          f32x16_t s[2][NT];
 #pragma unroll
-          for (int tb = 0; tb < 2; ++tb) {
-            f32x16_t s[NT];
+          for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) s[nt][i] = 0.0f;
-            const char* kp = kbuf + cur * kTileK + (32 * tb + m) * LDK + g * 16;
+              for (int i = 0; i < 16; ++i) s[tb][nt][i] = 0.0f;
+          const char* kp = kbuf + cur * kTileK + m * LDK + g * 16;
+          constexpr int kAhead = 6;        // reads of K ahead of the products that take them
+          Frag kf[2 * KS];
+          const auto read_k = [&](int i) {
+            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kp + 32 * (i & 1) * LDK + 32 * (i >> 1));
+            kf[i] = Frag{{w.x, w.y, w.z, w.w}};
+          };
 #pragma unroll
-            for (int c = 0; c < KS; ++c) {
-              const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kp + 32 * c);
-              const Frag kf = {{w.x, w.y, w.z, w.w}};
+          for (int i = 0; i < kAhead; ++i) read_k(i);
+          __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                s[nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf.get(), q[nt][c].get(), s[nt], 0, 0, 0);
-            }
-            if (edge) {
-              keep_branch();
+          for (int i = 0; i < 2 * KS; ++i) {
+            if (i + kAhead < 2 * KS) read_k(i + kAhead);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                int lo, hi;
-                limits(nt, &lo, &hi);
+            for (int nt = 0; nt < NT; ++nt)
+              s[i & 1][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i].get(), q[nt][i >> 1].get(), s[i & 1][nt], 0, 0, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, NT, 0);
+            if (i + kAhead < 2 * KS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
+          if (edge) {
+            keep_branch();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              int lo, hi;
+              limits(nt, &lo, &hi);
+#pragma unroll
+              for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const int t = tok + 32 * tb + 8 * (i >> 2) + 4 * g + (i & 3);
-                  if (!(t >= lo && t < min(hi, end))) s[nt][i] = -__builtin_inff();
+                  if (!(t >= lo && t < min(hi, end))) s[tb][nt][i] = -__builtin_inff();
                 }
-              }
             }
-            Frag pf[NT][2];
+          }
+          Frag pf[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float top = max3(s[nt][0], s[nt][1], s[nt][2]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float top = max3(s[0][nt][0], s[1][nt][0], s[0][nt][1]);
 #pragma unroll
-              for (int i = 3; i < 15; i += 2) top = max3(top, s[nt][i], s[nt][i + 1]);
-              top = max3(top, s[nt][15], s[nt][15]);
-              if (__builtin_amdgcn_ballot_w64(__builtin_fmaf(top, a.scale_log2, -run_m[nt]) > kSlack) != 0) {
-                keep_branch();
-                const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-                const float all = max3(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[1]));
-                const float nm = max3(run_m[nt], all * a.scale_log2, run_m[nt]);
-                const float alpha = __builtin_amdgcn_exp2f(run_m[nt] - nm);
-                run_m[nt] = nm;
-                run_l[nt] *= alpha;
+            for (int i = 1; i < 15; ++i) top = max3(top, s[1][nt][i], s[0][nt][i + 1]);
+            top = max3(top, s[1][nt][15], s[1][nt][15]);
+            if (__builtin_amdgcn_ballot_w64(__builtin_fmaf(top, a.scale_log2, -run_m[nt]) > kSlack) != 0) {
+              keep_branch();
+              const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+              const float all = max3(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[1]));
+              const float nm = max3(run_m[nt], all * a.scale_log2, run_m[nt]);
+              const float alpha = __builtin_amdgcn_exp2f(run_m[nt] - nm);
+              run_m[nt] = nm;
+              run_l[nt] *= alpha;
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) acc[nt][mb] *= alpha;
-              }
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][i], a.scale_log2, -run_m[nt]));
-                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][i + 1], a.scale_log2, -run_m[nt]));
-                const uint32_t w = pack2(x, y);
-                pf[nt][i >> 3].w[(i & 7) >> 1] = w;
-                run_l[nt] = add_pair(w, run_l[nt]);
-              }
+              for (int mb = 0; mb < MB; ++mb) acc[nt][mb] *= alpha;
             }
-            // out += V^T P^T. A transposing read gives 16 lanes four tokens of 16 channels: lane
-            // (m, g) holds tokens 4g .. 4g + 3 and 8 + 4g .. of channel m, as it holds of P
+          }
+          // out += V^T P^T. A transposing read gives 16 lanes four tokens of 16 channels: lane
+          // (m, g) holds tokens 4g .. 4g + 3 and 8 + 4g .. of channel m, as it holds of P
+          const char* vp = vbuf + cur * kTileV + (4 * g + ((lane & 15) >> 2)) * LDV + (16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              const char* vp = vbuf + cur * kTileV + (32 * tb + 16 * ks + 4 * g + ((lane & 15) >> 2)) * LDV +
-                               (16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
+          for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
-              for (int mb = 0; mb < MB; ++mb) {
-                const Frag vf = join4(read_transposed(vp + 64 * mb), read_transposed(vp + 64 * mb + 8 * LDV));
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  acc[nt][mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.get(), pf[nt][ks].get(), acc[nt][mb], 0, 0, 0);
+              for (int j = 0; j < 4; ++j) {
+                const int i = 8 * (ks & 1) + 2 * j;
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks >> 1][nt][i], a.scale_log2, -run_m[nt]));
+                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks >> 1][nt][i + 1], a.scale_log2, -run_m[nt]));
+                pf[nt][ks].w[j] = pack2(x, y);
+                run_l[nt] = add_pair(pf[nt][ks].w[j], run_l[nt]);
               }
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+              const char* p = vp + 16 * ks * LDV + 64 * mb;
+              const Frag vf = join4(read_transposed(p), read_transposed(p + 8 * LDV));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                acc[nt][mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.get(), pf[nt][ks].get(), acc[nt][mb], 0, 0, 0);
             }
           }
         }
@@ -817,9 +902,12 @@ template <class F, int D>
 AttendFn pick_wide(int row_tile) {
   if (row_tile == 1) return qknorm_attend_few<F, D, 1>;
   if (row_tile == 2) return qknorm_attend_few<F, D, 2>;
-  if (row_tile == 8) return qknorm_attend_many<F, D, 1>;
-  if constexpr (D < 256) {
-    if (row_tile == 16) return qknorm_attend_many<F, D, 2>;
+  if (row_tile == 8) return qknorm_attend_many<F, D, 1, 4>;
+  if constexpr (D == 64) {
+    if (row_tile == 16) return qknorm_attend_many<F, D, 2, 4>;
+  }
+  if constexpr (D == 128) {
+    if (row_tile == 16) return qknorm_attend_many<F, D, 1, 8>;
   }
   return nullptr;
 }
@@ -842,7 +930,8 @@ int launch_attend_wide(bool mx8, const AttendPlan& p, const AttendArgs& args, vo
   AttendArgs a = args;
   void* kargs[] = {&a};
   const int64_t grid = (int64_t)a.B * a.heads_k * a.row_tiles * a.splits;
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)grid), dim3(64 * kWaves),
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)grid),
+                                       dim3(p.head_dim == 128 && p.row_tile == 16 ? 512 : 64 * kWaves),
                                        kargs, 0, static_cast<hipStream_t>(stream));
   if (e == hipSuccess && a.splits > 1) return launch_attend_join(p, a, stream, err);
   if (e != hipSuccess) {
