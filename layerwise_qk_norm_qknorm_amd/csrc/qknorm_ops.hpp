@@ -53,7 +53,6 @@ struct RopePlan {
 constexpr int kMostAxes = 4;
 struct RopeAxes {
   int n;               // 0: one position a token
-  int mixed;           // 1: the angles of a lane's piece lie on different axes
   int64_t ld;
   uint32_t of[kRopeMaxHead / 2 / 16];
 };

@@ -86,19 +86,13 @@ int check_axes(const char* fn, const qknorm_rope_t* rope, const qknorm_axes_t* a
   return QKNORM_OK;
 }
 
-// What the kernels take of them. `angles` of a lane's piece go together where they
-// share an axis.
-void axes_args(const qknorm_rope_t* rope, const qknorm_axes_t* axes, int angles, RopeAxes* out) {
+// What the kernels take of them.
+void axes_args(const qknorm_rope_t* rope, const qknorm_axes_t* axes, RopeAxes* out) {
   if (!axes || !rope || !rope->rot_dim || axes->n_axes == 1) return;   // n == 0: one axis
   out->n = axes->n_axes;
   out->ld = axes->ld_positions;
-  for (int64_t i = 0; i < rope->rot_dim / 2; ++i) {
-    out->of[i >> 4] |= (uint32_t)axes->axis[i] << (2 * (i & 15));
-    if (axes->axis[i] != axes->axis[i - i % angles]) out->mixed = 1;
-  }
+  for (int64_t i = 0; i < rope->rot_dim / 2; ++i) out->of[i >> 4] |= (uint32_t)axes->axis[i] << (2 * (i & 15));
 }
-// Angles of a lane's piece: of a whole chunk, or of a pair of pieces.
-int angles_of(const RopePlan& p, bool inter) { return p.whole && inter ? p.vw / 2 : p.vw; }
 
 int check_width(const char* fn, const char* nm, int64_t h, int64_t head_dim) {
   if (h <= 0 || h % head_dim)
@@ -438,7 +432,7 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
   a.head_dim = (int)head_dim;
   a.pairs = p.pairs;
   table_args(rope, p, &a.rot, &a.rot_pairs, &a.cos_sin, &a.ld_table, &a.n_positions, &a.positions);
-  axes_args(rope, axes, angles_of(p, inter), &a.axes);
+  axes_args(rope, axes, &a.axes);
   a.log2_lanes = log2_of(p.lanes);
   a.half_lanes = rot && !inter ? (int)(rot / 2 / p.vw) : 0;
   a.idle = p.lanes * p.np * 2 * p.vw != head_dim;
@@ -595,7 +589,7 @@ int check_grad(const char* fn, const qknorm_grad_operand_t* q, const qknorm_grad
   a.head_dim = (int)head_dim;
   a.pairs = plan->pairs;
   table_args(rope, *plan, &a.rot, &a.rot_pairs, &a.cos_sin, &a.ld_table, &a.n_positions, &a.positions);
-  axes_args(rope, axes, angles_of(*plan, rot && rope->interleaved), &a.axes);
+  axes_args(rope, axes, &a.axes);
   a.log2_lanes = log2_of(plan->lanes);
   a.half_lanes = rot && !rope->interleaved ? (int)(rot / 2 / plan->vw) : 0;
   a.idle = plan->lanes * plan->np * 2 * plan->vw != head_dim;

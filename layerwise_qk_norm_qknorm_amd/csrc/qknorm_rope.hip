@@ -82,34 +82,48 @@ struct Chunk1 {
 // cos and sin for a lane's chunk at one position (half-split: the sine with
 // the sign its member takes). A position outside the table gives NaN, which
 // reaches every rotated column of the token.
-// AXES: positions on several axes, each angle from the row of its own.
-template <int VW, bool INTER, bool AXES>
+// AXES: positions on several axes, gathered by the wave and read from LDS.
+template <class IO, bool INTER, bool AXES>
 struct Turn {
+  static constexpr int VW = IO::kVW;
   static constexpr int TW = Chunk1<VW, INTER>::TW;
+  static constexpr int kRounds = AXES ? VW / 2 : 1;        // 64 lanes hold a head: at most 64 VW / 2 angles
+  static constexpr int kLds = AXES ? 2 * 64 * kRounds : 1;   // floats a wave
   float c[TW], s[TW];
-  uint32_t lost;     // AXES: bits of the angles that are NaN
+  AxisAngles own;
   bool in;
-  __device__ __forceinline__ void load(const float* table, int64_t ld, int64_t n, int64_t pos, int half, int tab) {
-    in = pos >= 0 && pos < n;
-    const float* row = table + (in ? pos : 0) * ld;
-    load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + tab), reinterpret_cast<uint32_t*>(c));
-    load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + half + tab), reinterpret_cast<uint32_t*>(s));
+  // A token's position or positions, to be loaded before its rows: the angles'
+  // addresses wait for them.
+  struct Where {
+    int64_t pos;
+    AxisAngles::Positions all;
+    template <class Args>
+    __device__ __forceinline__ void load(const Args& a, int64_t t) {
+      if constexpr (AXES)
+        all.load(a, t);
+      else
+        pos = load_uniform(a.positions + t);
+    }
+  };
+  template <class Args>
+  __device__ __forceinline__ void load(const Args& a, const Where& w, const Chunk1<VW, INTER>& at, uint32_t axes) {
+    if constexpr (AXES) {
+      own.load(a, w.all, axes);
+    } else {
+      in = w.pos >= 0 && w.pos < a.n_positions;
+      const float* row = a.cos_sin + (in ? w.pos : 0) * a.ld_table;
+      load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + at.tab), reinterpret_cast<uint32_t*>(c));
+      load_bytes<TW * 4, false>(reinterpret_cast<const char*>(row + (a.rot >> 1) + at.tab), reinterpret_cast<uint32_t*>(s));
+    }
   }
   template <class Args>
-  __device__ __forceinline__ void load(const Args& a, const Position<AXES>& pos, const Chunk1<VW, INTER>& at,
-                                       uint32_t axes) {
-    if constexpr (AXES)
-      lost = load_angles<TW>(axis_rows(a, pos), a.axes.mixed, axes, a.rot >> 1, at.tab, c, s);
-    else
-      load(a.cos_sin, a.ld_table, a.n_positions, pos.on[0], a.rot >> 1, at.tab);
-  }
-  __device__ __forceinline__ void settle(const Chunk1<VW, INTER>& at) {
+  __device__ __forceinline__ void settle(const Args& a, int64_t t, const Chunk1<VW, INTER>& at, float* lds) {
     if constexpr (AXES) {
-      if (__builtin_amdgcn_ballot_w64(lost != 0) != 0) {
-        keep_branch();
+      own.template put<kRounds>(a, t, lds);
 #pragma unroll
-        for (int e = 0; e < TW; ++e)
-          if (lost >> e & 1) c[e] = s[e] = __builtin_nanf("");
+      for (int e = 0; e < TW; ++e) {
+        c[e] = lds[at.tab + e];
+        s[e] = lds[kSinAt(kRounds) + at.tab + e];
       }
     } else if (!in) {
       keep_branch();
@@ -126,8 +140,8 @@ struct Turn {
 // Rotates a lane's chunk (BACK: by the opposite angle, the transposed map that
 // gradients take). half_lanes: lanes between the members of a pair. With MAG,
 // `mag` gets the magnitudes that each result is the sum of.
-template <bool BACK, bool MAG, class F, int VW, bool INTER, bool AXES>
-__device__ __forceinline__ void rotate_chunk(F (&z)[VW], const Turn<VW, INTER, AXES>& t, const Chunk1<VW, INTER>& at,
+template <bool BACK, bool MAG, class F, int VW, class IO, bool INTER, bool AXES>
+__device__ __forceinline__ void rotate_chunk(F (&z)[VW], const Turn<IO, INTER, AXES>& t, const Chunk1<VW, INTER>& at,
                                              int half_lanes, bool partial, float (&mag)[VW]) {
   F y[VW], p[VW];
   if constexpr (INTER) {
@@ -227,8 +241,8 @@ __device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float 
 // A lane's normalized and rotated chunk formed in float64 and rounded to odd,
 // four elements at a time to keep registers for waves.
 template <class IO, bool INTER, bool AXES>
-__device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, const char* gamma, const Position<AXES>& pos, bool turns,
-                                            const Chunk1<IO::kVW, INTER>& at, uint32_t axes, int L,
+__device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, const char* gamma, int64_t pos, bool turns,
+                                            const Chunk1<IO::kVW, INTER>& at, const float* lds, int L,
                                             float (&f)[IO::kVW]) {
   constexpr int VW = IO::kVW;
   constexpr int GB = VW * IO::kGBytes;
@@ -253,14 +267,9 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
   }
   bool in = false;
   const float* row = nullptr;
-  AxisRows rows;
-  if (turns) {
-    if constexpr (AXES) {
-      rows = axis_rows(a, pos);
-    } else {
-      in = pos.on[0] >= 0 && pos.on[0] < a.n_positions;
-      row = a.cos_sin + (in ? pos.on[0] : 0) * a.ld_table + at.tab;
-    }
+  if (!AXES && turns) {
+    in = pos >= 0 && pos < a.n_positions;
+    row = a.cos_sin + (in ? pos : 0) * a.ld_table + at.tab;
   }
 #pragma unroll 1
   for (int e0 = 0; e0 < VW; e0 += 4) {
@@ -288,12 +297,12 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = INTER ? (e0 + k) >> 1 : e0 + k;
+        double c, sn;
         if constexpr (AXES) {
-          const uint32_t axis = axes >> (2 * i) & 3;
-          row = rows.of(axis) + at.tab;
-          in = rows.in >> axis & 1;
+          c = lds[at.tab + i], sn = lds[kSinAt(Turn<IO, INTER, true>::kRounds) + at.tab + i];
+        } else {
+          c = in ? row[i] : __builtin_nanf(""), sn = in ? row[(a.rot >> 1) + i] : __builtin_nanf("");
         }
-        const double c = in ? row[i] : __builtin_nanf(""), sn = in ? row[(a.rot >> 1) + i] : __builtin_nanf("");
         const bool first = INTER ? (k & 1) == 0 : at.flip != 0;   // of its pair: the sine is subtracted
         const double y = z[k] * c + p[k] * (first ? -sn : sn);
         p[k] = at.turned ? y : z[k];
@@ -351,7 +360,10 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
   const Chunk1<VW, INTER> at(lane & (L - 1), a.rot, a.half_lanes);
   const bool partial = a.rot < a.head_dim;
   const bool turns = a.rot != 0 && c != 2;
-  const uint32_t axes = AXES ? axes_at(a.axes, at.tab) : 0;
+  using T = Turn<IO, INTER, AXES>;
+  __shared__ __align__(16) float angles[kRopeWaves * T::kLds];
+  float* const lds = angles + (threadIdx.x >> 6) * T::kLds;
+  const uint32_t axes = AXES && turns ? lane_axes(a.axes) : 0;
 
   const char* gamma = static_cast<const char*>(c == 2 ? nullptr : o.gamma);
   Piece<GB> gam;   // of the first slot: of all where heads share it
@@ -394,17 +406,17 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
     // A row that holds no token is worked like the others, and not stored: its
     // slot, waited for first, would hold up all that follows.
     int64_t place = 0;
-    Position<AXES> pos;
     if constexpr (MODE != ROPE_FORWARD) place = load_uniform(a.slots + t);
-    if (turns) pos.load(a, t);
+    typename T::Where where;
+    if (turns) where.load(a, t);
     Piece<16> x[S];
 #pragma unroll
     for (int i = 0; i < S; ++i)
       load_bytes<16, true>(static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + off[i], x[i].w);
-    Turn<VW, INTER, AXES> turn;
+    T turn;
     if (turns) {
-      turn.load(a, pos, at, axes);
-      turn.settle(at);
+      turn.load(a, where, at, axes);
+      turn.settle(a, t, at, lds);
     }
     const bool live = MODE == ROPE_FORWARD || (place >= 0 && place < a.n_tokens_held);
 
@@ -473,7 +485,7 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
         exact_chunk<IO, INTER, AXES>(
             a, static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + (int64_t)((on ? head : 0) * a.head_dim + at.col) * IO::kBytes,
             gamma ? gamma + ((on ? head : 0) * a.gstride + at.col) * IO::kGBytes : nullptr,
-            pos, turns, at, axes, L, f);
+            where.pos, turns, at, lds, L, f);
         const Coded<MX, VW> q = quantize<MX, VW>(f);
         store(i, on, f, q, t, place);
       }
@@ -510,7 +522,10 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
   const int hc = on ? head : 0;
   const Chunk1<VW, INTER> at(lane & (L - 1), a.rot, a.half_lanes);
   const bool partial = a.rot < a.head_dim;
-  const uint32_t axes = AXES ? axes_at(a.axes, at.tab) : 0;
+  using T = Turn<IO, INTER, AXES>;
+  __shared__ __align__(16) float angles[kGradWaves * T::kLds];
+  float* const lds = angles + wave * T::kLds;
+  const uint32_t axes = AXES ? lane_axes(a.axes) : 0;
   const uint32_t off = (uint32_t)(hc * a.head_dim + at.col) * IO::kBytes;
 
   float g[VW], sum[VW];
@@ -524,15 +539,15 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
 
   struct In {
     Piece<16> x, dy;
-    Turn<VW, INTER, AXES> turn;
+    T turn;
   };
   const auto load = [&](In& in, int64_t t) {
     load_bytes<16, true>(static_cast<const char*>(o.x) + t * o.ldx * IO::kBytes + off, in.x.w);
     load_bytes<16, true>(static_cast<const char*>(o.dy) + t * o.lddy * IO::kBytes + off, in.dy.w);
     if (a.rot) {
-      Position<AXES> pos;
-      pos.load(a, t);
-      in.turn.load(a, pos, at, axes);
+      typename T::Where where;
+      where.load(a, t);
+      in.turn.load(a, where, at, axes);
     }
   };
   const auto work = [&](In& in, int64_t t) {
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
     widen<IO, VW>(in.x.w, x);
     widen<IO, VW>(in.dy.w, y);
     if (a.rot) {
-      in.turn.settle(at);
+      in.turn.settle(a, t, at, lds);
       rotate_chunk<true, false>(y, in.turn, at, a.half_lanes, partial, gg);
     }
     float ss = 0.0f, dot = 0.0f;

@@ -141,69 +141,103 @@ __device__ __forceinline__ void narrow(const float (&v)[VW], uint32_t* w) {
   }
 }
 
-// The rows of the angle table that a token's positions on several axes name,
-// the same for the whole wave. A position outside the table reads row 0, and its
-// angles become NaN.
-struct AxisRows {
-  uint64_t row0, row1, row2, row3;   // (an array would be chosen from in memory)
-  uint32_t in;                       // bit x: the position on axis x lies in the table
-  __device__ __forceinline__ const float* of(uint32_t axis) const {
-    const uint64_t lo = axis & 1 ? row1 : row0, hi = axis & 1 ? row3 : row2;
-    return reinterpret_cast<const float*>(axis & 2 ? hi : lo);
-  }
-};
-static_assert(kMostAxes == 4, "AxisRows");
-// A token's position, or AXES: its positions (axes there are not: the first).
-template <bool AXES>
-struct Position {
-  int64_t on[AXES ? kMostAxes : 1];
-  template <class Args>
-  __device__ __forceinline__ void load(const Args& a, int64_t t) {
-    on[0] = load_uniform(a.positions + t);
-    if constexpr (AXES) {
+// Positions on several axes. A wave gathers its token's angles, a lane's each
+// (lane + 64 r), from the rows that their axes' positions name, and lays them side
+// by side in LDS, where its lanes then read them as they would a row of the table:
+// two loads of 4 bytes a lane instead of its chunk's angles for each lane, whatever
+// the order of the axes (8192 tokens of 40 + 8 bf16 heads of 128: sections 43.2 ->
+// AXES_S us, axes in turn 63 -> AXES_T; a single position, loaded as chunks, 37.0).
+// Angles past the first 128 are gathered when they are laid down, so that they
+// take no registers (rotations of more than 256 columns).
+constexpr int kSinAt(int rounds) { return 64 * rounds; }     // floats; rounds: 64 angles each
+constexpr int kHeldRounds = 2;
+struct AxisAngles {
+  float c[kHeldRounds], s[kHeldRounds];
+  uint32_t lost;       // bits of the angles whose position lies outside the table: NaN
+
+  struct Rows {        // (in an array they would be chosen from in memory)
+    uint64_t row0, row1, row2, row3;
+    uint32_t in;
+  };
+  static_assert(kMostAxes == 4, "Rows");
+  struct Positions {
+    int64_t on[kMostAxes];      // axes there are not: the first one's
+    template <class Args>
+    __device__ __forceinline__ void load(const Args& a, int64_t t) {
 #pragma unroll
-      for (int x = 1; x < kMostAxes; ++x) on[x] = load_uniform(a.positions + (x < a.axes.n ? x : 0) * a.axes.ld + t);
+      for (int x = 0; x < kMostAxes; ++x) on[x] = load_uniform(a.positions + (x < a.axes.n ? x : 0) * a.axes.ld + t);
+    }
+  };
+  template <class Args>
+  __device__ __forceinline__ static Rows rows(const Args& a, const Positions& pos) {
+    Rows w;
+    w.in = 0;
+    const auto row = [&](int x) {
+      const bool ok = pos.on[x] >= 0 && pos.on[x] < a.n_positions;
+      w.in |= (uint32_t)ok << x;
+      return uniform64(reinterpret_cast<uint64_t>(a.cos_sin + (ok ? pos.on[x] : 0) * a.ld_table));
+    };
+    w.row0 = row(0), w.row1 = row(1), w.row2 = row(2), w.row3 = row(3);
+    return w;
+  }
+  // Angle j (past the last: the first), on axis x.
+  __device__ __forceinline__ static bool fetch(const Rows& w, uint32_t x, int j, int half, float& c, float& s) {
+    const uint64_t lo = x & 1 ? w.row1 : w.row0, hi = x & 1 ? w.row3 : w.row2;
+    const float* p = reinterpret_cast<const float*>(x & 2 ? hi : lo) + (j < half ? j : 0);
+    c = p[0];
+    s = p[half];
+    return w.in >> x & 1;
+  }
+  // axis: lane_axes
+  template <class Args>
+  __device__ __forceinline__ void load(const Args& a, const Positions& pos, uint32_t axis) {
+    const Rows w = rows(a, pos);
+    const int half = a.rot >> 1, lane = threadIdx.x & 63;
+    lost = 0;
+#pragma unroll
+    for (int r = 0; r < kHeldRounds; ++r) {
+      c[r] = s[r] = 0.0f;
+      if (64 * r < half) lost |= (uint32_t)!fetch(w, axis >> (2 * r) & 3, lane + 64 * r, half, c[r], s[r]) << r;
     }
   }
-};
-template <class Args>
-__device__ __forceinline__ AxisRows axis_rows(const Args& a, const Position<true>& pos) {
-  AxisRows r;
-  r.in = 0;
-  const auto row = [&](int x) {
-    const bool in = pos.on[x] >= 0 && pos.on[x] < a.n_positions;
-    r.in |= (uint32_t)in << x;
-    return uniform64(reinterpret_cast<uint64_t>(a.cos_sin + (in ? pos.on[x] : 0) * a.ld_table));
-  };
-  r.row0 = row(0), r.row1 = row(1), r.row2 = row(2), r.row3 = row(3);
-  return r;
-}
-// The axes of the angles from `tab` on, two bits each (a piece's angles share a word).
-__device__ __forceinline__ uint32_t axes_at(const RopeAxes& axes, int tab) {
-  return axes.of[tab >> 4] >> (2 * (tab & 15));
-}
-// cos and sin of N angles from `tab` on, each from the row of its axis, with wide
-// loads where they share one. Returns a bit for each angle of a position outside
-// the table.
-template <int N>
-__device__ __forceinline__ uint32_t load_angles(const AxisRows& rows, bool mixed, uint32_t axes, int half, int tab,
-                                                float (&c)[N], float (&s)[N]) {
-  if (!mixed) {
-    const float* row = rows.of(axes & 3) + tab;
-    load_bytes<N * 4, false>(reinterpret_cast<const char*>(row), reinterpret_cast<uint32_t*>(c));
-    load_bytes<N * 4, false>(reinterpret_cast<const char*>(row + half), reinterpret_cast<uint32_t*>(s));
-    return rows.in >> (axes & 3) & 1 ? 0u : ~0u;
-  }
-  uint32_t lost = 0;
+  template <int ROUNDS, class Args>
+  __device__ __forceinline__ void put(const Args& a, int64_t t, float* lds) const {
+    const int half = a.rot >> 1, lane = threadIdx.x & 63;
+    const float nan = __builtin_nanf("");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const uint32_t axis = axes >> (2 * e) & 3;
-    const float* row = rows.of(axis) + tab + e;
-    c[e] = row[0];
-    s[e] = row[half];
-    lost |= (~rows.in >> axis & 1) << e;
+    for (int r = 0; r < kHeldRounds; ++r)
+      if (r < ROUNDS && 64 * r < half) {
+        lds[lane + 64 * r] = lost >> r & 1 ? nan : c[r];
+        lds[kSinAt(ROUNDS) + lane + 64 * r] = lost >> r & 1 ? nan : s[r];
+      }
+    if (ROUNDS > kHeldRounds && half > 64 * kHeldRounds) {
+      keep_branch();
+      Positions pos;
+      pos.load(a, t);
+      const Rows w = rows(a, pos);
+#pragma unroll 1
+      for (int j = lane + 64 * kHeldRounds; j - lane < half; j += 64) {
+        float cj, sj;
+        const bool in = fetch(w, a.axes.of[j >> 4] >> (2 * (j & 15)) & 3, j, half, cj, sj);
+        lds[j] = in ? cj : nan;
+        lds[kSinAt(ROUNDS) + j] = in ? sj : nan;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
-  return lost;
+};
+// The axes of a lane's held angles, two bits each.
+__device__ __forceinline__ uint32_t lane_axes(const RopeAxes& axes) {
+  uint32_t own = 0;
+#pragma unroll
+  for (int r = 0; r < kHeldRounds; ++r) {
+    const int j = (threadIdx.x & 63) + 64 * r;
+    own |= (axes.of[j >> 4] >> (2 * (j & 15)) & 3) << (2 * r);
+  }
+  return own;
 }
 
 // The formats of quantised caches. A block of 32 channels has the scale 2^E, E =

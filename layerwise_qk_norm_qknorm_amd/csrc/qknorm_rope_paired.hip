@@ -66,29 +66,30 @@ __device__ __forceinline__ void drop_idle(Piece<PB> (&a)[NP], Piece<PB> (&b)[NP]
 template <int VW, int NP, bool INTER, bool AXES>
 struct Angles {
   float c[NP][VW], s[NP][VW];
-  // of token t; AXES: positions on several axes, each angle from the row of its own
+  // AXES: positions on several axes, gathered by the wave and read from LDS
+  static constexpr int kRounds = AXES ? kRopeMaxHead / 2 / 64 : 1;
+  static constexpr int kLds = AXES ? 2 * 64 * kRounds : 1;   // floats a wave
+  AxisAngles own;
   template <class Args>
-  __device__ __forceinline__ void load(const Args& a, int64_t t, const Place<VW, NP, INTER>& at) {
+  __device__ __forceinline__ void load(const Args& a, int64_t t, const Place<VW, NP, INTER>& at, uint32_t axes) {
     if constexpr (AXES) {
-      Position<true> pos;
+      AxisAngles::Positions pos;
       pos.load(a, t);
-      const AxisRows rows = axis_rows(a, pos);
-      uint32_t lost[NP], any = 0;
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        lost[k] = load_angles<VW>(rows, a.axes.mixed, axes_at(a.axes, at.tab[k]), a.rot >> 1, at.tab[k], c[k], s[k]);
-        any |= lost[k];
-      }
-      if (__builtin_amdgcn_ballot_w64(any != 0) != 0) {
-        keep_branch();
-#pragma unroll
-        for (int k = 0; k < NP; ++k)
-#pragma unroll
-          for (int e = 0; e < VW; ++e)
-            if (lost[k] >> e & 1) c[k][e] = s[k][e] = __builtin_nanf("");
-      }
-    } else {
+      own.load(a, pos, axes);
+    } else
       load(a.cos_sin, a.ld_table, a.n_positions, load_uniform(a.positions + t), a.rot >> 1, at);
+  }
+  template <class Args>
+  __device__ __forceinline__ void settle(const Args& a, int64_t t, float* lds, const Place<VW, NP, INTER>& at) {
+    if constexpr (AXES) {
+      own.template put<kRounds>(a, t, lds);
+#pragma unroll
+      for (int k = 0; k < NP; ++k)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          c[k][e] = lds[at.tab[k] + e];
+          s[k][e] = lds[kSinAt(kRounds) + at.tab[k] + e];
+        }
     }
   }
   __device__ __forceinline__ void load(const float* table, int64_t ld, int64_t n, int64_t pos, int half,
@@ -217,6 +218,11 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
   const int hw = 64 >> a.log2_lanes;
   const Place<VW, NP, INTER> at(lane & (L - 1), L, a.pairs, a.rot_pairs, a.rot, a.head_dim);
 
+  using Turns = Angles<VW, NP, INTER, AXES>;
+  __shared__ __align__(16) float angles[kRopeMaxWaves * Turns::kLds];
+  float* const lds = angles + wave * Turns::kLds;
+  const uint32_t axes = AXES ? lane_axes(a.axes) : 0;
+
   // What the wave's slots hold, the same for all its tokens: the side (Q, K or
   // V), the lane's byte offset in its rows, and gamma.
   int side[S];
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
 
   struct In {   // one token
     Piece<PB> xa[S][NP], xb[S][NP];
-    Angles<VW, NP, INTER, AXES> turn;
+    Turns turn;
     int64_t place;
   };
   const auto load = [&](In& in, int64_t t) {
@@ -259,11 +265,12 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
         load_bytes<PB, true>(row + ob[i][k], in.xb[i][k].w);
       }
     }
-    if (a.rot_pairs) in.turn.load(a, t, at);
+    if (a.rot_pairs) in.turn.load(a, t, at, axes);
   };
 
   const auto work = [&](In& in, int64_t t) {
     if (MODE != ROPE_FORWARD && (in.place < 0 || in.place >= a.n_tokens_held)) return;   // a row that holds no token
+    if (a.rot_pairs) in.turn.settle(a, t, lds, at);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int s = slot0 + i;
@@ -421,6 +428,11 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
   const int hc = on ? head : 0;
   const Place<VW, NP, INTER> at(lane & (L - 1), L, a.pairs, a.rot_pairs, a.rot, a.head_dim);
 
+  using Turns = Angles<VW, NP, INTER, AXES>;
+  __shared__ __align__(16) float angles[kGradWaves * Turns::kLds];
+  float* const lds = angles + wave * Turns::kLds;
+  const uint32_t axes = AXES ? lane_axes(a.axes) : 0;
+
   float gfa[NP][VW], gfb[NP][VW];
   float sa[NP][VW], sb[NP][VW];
   uint32_t oa[NP], ob[NP];
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
 
   struct In {
     Piece<PB> xa[NP], xb[NP], ya[NP], yb[NP];
-    Angles<VW, NP, INTER, AXES> turn;
+    Turns turn;
   };
   const auto load = [&](In& in, int64_t t) {
     const char* xr = x + t * o.ldx * IO::kBytes;
@@ -457,9 +469,10 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
       load_bytes<PB, true>(yr + oa[k], in.ya[k].w);
       load_bytes<PB, true>(yr + ob[k], in.yb[k].w);
     }
-    if (a.rot_pairs) in.turn.load(a, t, at);
+    if (a.rot_pairs) in.turn.load(a, t, at, axes);
   };
   const auto work = [&](In& in, int64_t t) {
+    if (a.rot_pairs) in.turn.settle(a, t, lds, at);
     if (a.idle) {
       keep_branch();
       drop_idle<PB, VW, NP, INTER>(in.xa, in.xb, at);
