@@ -18,9 +18,9 @@
 // Two kernels. qknorm_attend_few, for up to 32 rows of a sequence and key head:
 // the four waves of a block take the 32-token tiles of its part of the cache in
 // turn, K straight into registers, and join in LDS at the end; bound by the
-// cache's bytes. qknorm_attend_many, beyond: each wave takes 32 or 64 rows of its
-// own, and all share K and V tiles of 64 tokens that the block stages in LDS;
-// bound by the matrix unit.
+// cache's bytes. qknorm_attend_many, beyond: each wave takes 32 rows of its own, and
+// all share K and V tiles of 64 tokens that the block stages in LDS;
+// bound by the matrix and the vector unit.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -577,21 +577,23 @@ __device__ __forceinline__ Work work_of(const AttendArgs& a, int block_rows) {
   return w;
 }
 
-// NT tiles of 32 rows a wave. K and V tiles of kTok tokens in LDS, two of each:
+// NW waves of 32 rows each. K and V tiles of kTok tokens in LDS, two of each:
 // one is read while the next one, loaded into registers behind the products,
 // waits to be written.
-template <class F, int D, int NT, int NW>
-__global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qknorm_attend_many(const AttendArgs a) {
-  constexpr int kTok = 64;
+template <class F, int D, int NW>
+__global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknorm_attend_many(const AttendArgs a) {
+  constexpr int TB = 2;                      // 32-token parts of a tile
+  constexpr int kTok = 32 * TB;
   constexpr int MB = D / 32;                 // 32-channel blocks of the output
   constexpr int KS = D / 16;                 // steps of the first product
   constexpr int kPer = D / F::kVW;           // lanes across a token
   constexpr int kAt = 64 / kPer;             // tokens of one wave's load
-  constexpr int PL = kTok / (NW * kAt);  // loads a thread makes of K, and of V
+  constexpr int PL = (kTok + NW * kAt - 1) / (NW * kAt);   // loads a thread makes of K, and of V
   constexpr int LDK = D * 2 + 16, LDV = D * 2 + 64;   // bytes of a row: no two of those read together share a bank
-  constexpr int kBlock = 32 * NT * NW;   // rows of a block
+  constexpr int kBlock = 32 * NW;   // rows of a block
   constexpr int kTileK = kTok * LDK, kTileV = kTok * LDV;
-  constexpr int LDO = D + 4;                 // padded row of the results on their way out
+  constexpr int kOut = D < 128 ? D : 128;    // columns of the results on their way out at a time
+  constexpr int LDO = kOut + 4;
   constexpr int kTiles = 2 * (kTileK + kTileV), kResults = NW * 32 * LDO * 4;
   __shared__ __align__(16) char lds[kTiles > kResults ? kTiles : kResults];
   char* const kbuf = lds;
@@ -613,6 +615,7 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
   const int heads_q = a.heads_k * a.group;
   const uint32_t off = (lane / kPer) * (uint32_t)a.token_stride + (lane % kPer) * 16;
   const uint32_t s_off = (lane / kPer) * (D / 32) + (lane % kPer) / 2;
+  const bool loads = NW * kAt <= kTok || wave * kAt < kTok;      // a tile of 64 MXFP8 columns is less than eight waves load at a time
 
   for (int b0 = grid_tile * kBlock; b0 < rows; b0 += a.row_tiles * kBlock) {
     const int i_first = over(b0, a.by_group);
@@ -622,22 +625,21 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
     if (split > 0 && split >= sp.chunks) continue;
     const int block_lo = see_lo(a, seq, i_last), block_hi = see_hi(a, seq, i_first);   // every row of the block sees these
     // this wave's rows: [r0, r1), what they see together and each
-    const int r0 = b0 + wave * (32 * NT), r1 = min(rows, r0 + 32 * NT);
+    const int r0 = b0 + wave * 32, r1 = min(rows, r0 + 32);
     const bool live = r0 < rows;
     const int w_first = live ? (int)over(r0, a.by_group) : 0, w_last = live ? (int)over(r1 - 1, a.by_group) : 0;
     const int any_lo = see_lo(a, seq, w_first), any_hi = live ? see_hi(a, seq, w_last) : 0;
-    const int lo_all = see_lo(a, seq, w_last), hi_all = r1 - r0 == 32 * NT ? see_hi(a, seq, w_first) : 0;
+    const int lo_all = see_lo(a, seq, w_last), hi_all = r1 - r0 == 32 ? see_hi(a, seq, w_first) : 0;
 
-    const auto limits = [&](int nt, int* lo, int* hi) {
-      const int r = r0 + nt * 32 + m;
+    const auto limits = [&](int* lo, int* hi) {
+      const int r = r0 + m;
       const int i = r < rows ? (int)over(r, a.by_group) : 0;
       *lo = see_lo(a, seq, i);
       *hi = r < rows ? see_hi(a, seq, i) : 0;
     };
-    Frag q[NT][KS];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 32 + m;
+    Frag q[KS];
+    {
+      const int r = r0 + m;
       const bool on = r < rows;
       const int i = on ? (int)over(r, a.by_group) : 0;
       const int head = hk * a.group + (on ? r - i * a.group : 0);
@@ -646,21 +648,16 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
       for (int c = 0; c < KS; ++c) {
         u32x4_t w = {0, 0, 0, 0};
         if (on) w = *reinterpret_cast<const u32x4_t*>(p + (16 * c + 8 * g) * 2);
-        q[nt][c] = Frag{{w.x, w.y, w.z, w.w}};
+        q[c] = Frag{{w.x, w.y, w.z, w.w}};
       }
     }
     if (threadIdx.x == 0) unusual = 0;
-    float run_m[NT], run_l[NT];
-    f32x16_t acc[NT][MB];
+    float run_m = kNothing, run_l = 0.0f;
+    f32x16_t acc[MB];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      run_m[nt] = kNothing;
-      run_l[nt] = 0.0f;
+    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[nt][mb][i] = 0.0f;
-    }
+      for (int i = 0; i < 16; ++i) acc[mb][i] = 0.0f;
 
     for (int ch = split; ch < sp.chunks; ch += a.splits) {
       const int begin = sp.first + ch * a.chunk;
@@ -674,6 +671,7 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
       int ids = pages_from(begin), ids_from = begin, ids_next = pages_from(begin + 1024);
       // this wave's share of a tile: tokens (x * NW + wave) * kAt and on
       const auto load = [&](int tok) {
+        if (!loads) return;
         if (tok >= ids_from + 1024) {
           ids_from += 1024;
           ids = ids_next;
@@ -698,6 +696,7 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
       };
       const int put_k = lane / kPer * LDK + lane % kPer * (F::kVW * 2), put_v = lane / kPer * LDV + lane % kPer * (F::kVW * 2);
       const auto store = [&](int tok, int buf) {
+        if (!loads) return;
         const bool edge = tok < block_lo || tok + kTok > min(block_hi, end);
         uint32_t top = 0;
         if constexpr (F::kCodes) {
@@ -750,88 +749,77 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
           const bool edge = tok < lo_all || tok + kTok > min(hi_all, end);
           // scores of both 32-token halves, transposed: lane (m, g) gets tokens
           // 32 tb + 8 (i / 4) + 4g + i % 4 of row m
-          f32x16_t s[2][NT];
+          f32x16_t s[TB];
 #pragma unroll
-          for (int tb = 0; tb < 2; ++tb)
+          for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) s[tb][nt][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
           const char* kp = kbuf + cur * kTileK + m * LDK + g * 16;
-          constexpr int kAhead = 6;        // reads of K ahead of the products that take them
-          Frag kf[2 * KS];
+          // reads of K ahead of the products that take them, which the compiler would
+          // otherwise wait for two by two
+          constexpr int kAhead = D == 64 ? 4 : 6;
+          Frag kf[TB * KS];
           const auto read_k = [&](int i) {
-            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kp + 32 * (i & 1) * LDK + 32 * (i >> 1));
+            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kp + 32 * (i % TB) * LDK + 32 * (i / TB));
             kf[i] = Frag{{w.x, w.y, w.z, w.w}};
           };
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) read_k(i);
-          __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);   // LDS reads
 #pragma unroll
-          for (int i = 0; i < 2 * KS; ++i) {
-            if (i + kAhead < 2 * KS) read_k(i + kAhead);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              s[i & 1][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i].get(), q[nt][i >> 1].get(), s[i & 1][nt], 0, 0, 0);
-            __builtin_amdgcn_sched_group_barrier(0x8, NT, 0);
-            if (i + kAhead < 2 * KS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          for (int i = 0; i < TB * KS; ++i) {
+            if (i + kAhead < TB * KS) read_k(i + kAhead);
+            s[i % TB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i].get(), q[i / TB].get(), s[i % TB], 0, 0, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);        // a product
+            if (i + kAhead < TB * KS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
           }
           if (edge) {
             keep_branch();
+            int lo, hi;
+            limits(&lo, &hi);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              int lo, hi;
-              limits(nt, &lo, &hi);
+            for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-              for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int t = tok + 32 * tb + 8 * (i >> 2) + 4 * g + (i & 3);
-                  if (!(t >= lo && t < min(hi, end))) s[tb][nt][i] = -__builtin_inff();
-                }
-            }
+              for (int i = 0; i < 16; ++i) {
+                const int t = tok + 32 * tb + 8 * (i >> 2) + 4 * g + (i & 3);
+                if (!(t >= lo && t < min(hi, end))) s[tb][i] = -__builtin_inff();
+              }
           }
-          Frag pf[NT][4];
+          // the lane's own largest score decides; the row's, over its two lanes, is needed when it moves
+          float top = s[0][0];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float top = max3(s[0][nt][0], s[1][nt][0], s[0][nt][1]);
+          for (int i = 1; i < 16 * TB; i += 2)
+            top = max3(top, s[i / 16][i % 16], s[(i + 1) / 16 % TB][(i + 1) % 16]);
+          if (__builtin_amdgcn_ballot_w64(__builtin_fmaf(top, a.scale_log2, -run_m) > kSlack) != 0) {
+            keep_branch();
+            const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+            const float all = max3(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[1]));
+            const float nm = max3(run_m, all * a.scale_log2, run_m);
+            const float alpha = __builtin_amdgcn_exp2f(run_m - nm);
+            run_m = nm;
+            run_l *= alpha;
 #pragma unroll
-            for (int i = 1; i < 15; ++i) top = max3(top, s[1][nt][i], s[0][nt][i + 1]);
-            top = max3(top, s[1][nt][15], s[1][nt][15]);
-            if (__builtin_amdgcn_ballot_w64(__builtin_fmaf(top, a.scale_log2, -run_m[nt]) > kSlack) != 0) {
-              keep_branch();
-              const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-              const float all = max3(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[1]));
-              const float nm = max3(run_m[nt], all * a.scale_log2, run_m[nt]);
-              const float alpha = __builtin_amdgcn_exp2f(run_m[nt] - nm);
-              run_m[nt] = nm;
-              run_l[nt] *= alpha;
-#pragma unroll
-              for (int mb = 0; mb < MB; ++mb) acc[nt][mb] *= alpha;
-            }
+            for (int mb = 0; mb < MB; ++mb) acc[mb] *= alpha;
           }
           // out += V^T P^T. A transposing read gives 16 lanes four tokens of 16 channels: lane
           // (m, g) holds tokens 4g .. 4g + 3 and 8 + 4g .. of channel m, as it holds of P
           const char* vp = vbuf + cur * kTileV + (4 * g + ((lane & 15) >> 2)) * LDV + (16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
+          for (int ks = 0; ks < 2 * TB; ++ks) {
+            Frag pf;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int i = 8 * (ks & 1) + 2 * j;
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks >> 1][nt][i], a.scale_log2, -run_m[nt]));
-                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks >> 1][nt][i + 1], a.scale_log2, -run_m[nt]));
-                pf[nt][ks].w[j] = pack2(x, y);
-                run_l[nt] = add_pair(pf[nt][ks].w[j], run_l[nt]);
-              }
+            for (int j = 0; j < 4; ++j) {
+              const int i = 8 * (ks & 1) + 2 * j;
+              const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks >> 1][i], a.scale_log2, -run_m));
+              const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks >> 1][i + 1], a.scale_log2, -run_m));
+              pf.w[j] = pack2(x, y);
+              run_l = add_pair(pf.w[j], run_l);
+            }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
               const char* p = vp + 16 * ks * LDV + 64 * mb;
               const Frag vf = join4(read_transposed(p), read_transposed(p + 8 * LDV));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                acc[nt][mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.get(), pf[nt][ks].get(), acc[nt][mb], 0, 0, 0);
+              acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.get(), pf.get(), acc[mb], 0, 0, 0);
             }
           }
         }
@@ -840,32 +828,34 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
       }
     }
 
-    // Out through LDS, 32 rows of each wave at a time: lane (m, g) holds row m, channels
-    // 32 mb + 8 (i / 4) + 4g + i % 4, and stores eight neighbouring ones of a row.
+    // Out through LDS, 32 rows of each wave at a time and at most 128 columns: lane (m, g)
+    // holds row m, channels 32 mb + 8 (i / 4) + 4g + i % 4, and stores eight neighbouring
+    // ones of a row.
     float* const res = reinterpret_cast<float*>(lds) + wave * 32 * LDO;
-    constexpr int kAcross = D / 8;           // lanes across a row
+    constexpr int kAcross = kOut / 8;        // lanes across a row
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float sum = swap_add32(run_l[nt]);
-      const float top = run_m[nt];
+    for (int mb0 = 0; mb0 < MB; mb0 += kOut / 32) {
+      const float sum = swap_add32(run_l);
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+      for (int mb = 0; mb < kOut / 32; ++mb)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x) {
+          const f32x16_t& o = acc[mb0 + mb];
           *reinterpret_cast<f32x4_t*>(res + m * LDO + 32 * mb + 8 * x + 4 * g) =
-              f32x4_t{acc[nt][mb][4 * x], acc[nt][mb][4 * x + 1], acc[nt][mb][4 * x + 2], acc[nt][mb][4 * x + 3]};
+              f32x4_t{o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]};
+        }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
       for (int y = 0; y < 32; y += 64 / kAcross) {
-        const int row = y + lane / kAcross, col = (lane % kAcross) * 8;
-        const int r = r0 + nt * 32 + row;
-        const float l = __shfl(sum, row), rm = __shfl(top, row);
+        const int row = y + lane / kAcross, at = (lane % kAcross) * 8, col = 32 * mb0 + at;
+        const int r = r0 + row;
+        const float l = __shfl(sum, row), rm = __shfl(run_m, row);
         if (r >= rows) continue;
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
-          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(res + row * LDO + col + e);
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(res + row * LDO + at + e);
           o[e] = v[0], o[e + 1] = v[1], o[e + 2] = v[2], o[e + 3] = v[3];
         }
         const int i = over(r, a.by_group);
@@ -875,11 +865,11 @@ __global__ void __launch_bounds__(64 * NW, NT * D <= 128 && NW == 4 ? 2 : 1) qkn
           add_unusual<F, kTok>(a, vsrc, table, sp, split, block_lo, block_hi, see_lo(a, seq, i), see_hi(a, seq, i), col, o);
         }
         if (joined) {
-          const int64_t at = ((int64_t)(seq.q0 + i) * heads_q + head) * a.splits + split;
-          float* p = a.part_o + at * D + col;
+          const int64_t part_at = ((int64_t)(seq.q0 + i) * heads_q + head) * a.splits + split;
+          float* p = a.part_o + part_at * D + col;
           *reinterpret_cast<f32x4_t*>(p) = f32x4_t{o[0], o[1], o[2], o[3]};
           *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{o[4], o[5], o[6], o[7]};
-          if (col == 0) *reinterpret_cast<f32x2_t*>(a.part_ml + at * 2) = f32x2_t{rm, l};
+          if (col == 0) *reinterpret_cast<f32x2_t*>(a.part_ml + part_at * 2) = f32x2_t{rm, l};
         } else {
           const bool empty = see_hi(a, seq, i) <= see_lo(a, seq, i);      // a row that sees nothing is zero
           const float inv = 1.0f / l;
@@ -902,12 +892,9 @@ template <class F, int D>
 AttendFn pick_wide(int row_tile) {
   if (row_tile == 1) return qknorm_attend_few<F, D, 1>;
   if (row_tile == 2) return qknorm_attend_few<F, D, 2>;
-  if (row_tile == 8) return qknorm_attend_many<F, D, 1, 4>;
-  if constexpr (D == 64) {
-    if (row_tile == 16) return qknorm_attend_many<F, D, 2, 4>;
-  }
+  if (row_tile == 8) return qknorm_attend_many<F, D, 4>;
   if constexpr (D == 128) {
-    if (row_tile == 16) return qknorm_attend_many<F, D, 1, 8>;
+    if (row_tile == 16) return qknorm_attend_many<F, D, 8>;
   }
   return nullptr;
 }
@@ -931,7 +918,7 @@ int launch_attend_wide(bool mx8, const AttendPlan& p, const AttendArgs& args, vo
   void* kargs[] = {&a};
   const int64_t grid = (int64_t)a.B * a.heads_k * a.row_tiles * a.splits;
   const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)grid),
-                                       dim3(p.head_dim == 128 && p.row_tile == 16 ? 512 : 64 * kWaves),
+                                       dim3(p.row_tile == 16 ? 512 : 64 * kWaves),
                                        kargs, 0, static_cast<hipStream_t>(stream));
   if (e == hipSuccess && a.splits > 1) return launch_attend_join(p, a, stream, err);
   if (e != hipSuccess) {

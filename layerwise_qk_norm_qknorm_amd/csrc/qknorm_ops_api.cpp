@@ -672,9 +672,9 @@ AttendPlan plan_attend_wide(int64_t head_dim, int64_t heads_k, int64_t group, in
   AttendPlan p;
   p.head_dim = (int)head_dim;
   const int64_t rows = max_q * group;
-  p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 128 || head_dim == 256 ? 8 : 16;
+  p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 128 || head_dim != 128 ? 8 : 16;
   const int64_t tiles = (rows + 16 * p.row_tile - 1) / (16 * p.row_tile);
-  const int64_t resident = 256 * (head_dim == 256 || (p.row_tile == 16 && head_dim == 128) ? 1 : 2);
+  const int64_t resident = 256 * (head_dim == 256 || p.row_tile == 16 ? 1 : 2);
   p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);
   p.max_q = max_q;
   const int64_t blocks = B * heads_k * p.row_tiles;
