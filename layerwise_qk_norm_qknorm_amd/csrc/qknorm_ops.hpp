@@ -84,7 +84,6 @@ struct RopeArgs {
   const float* cos_sin;
   int64_t ld_table, n_positions;
   const int64_t* positions;
-  RopeAxes axes;
   float inv_div, eps;
   // appending only
   const int64_t* slots;
@@ -97,12 +96,16 @@ struct RopeArgs {
   int y_wide;              // 1: the rows for cached values take 16-byte stores
 };
 
+struct RopeAxesArgs : RopeArgs {   // of the kernels for several axes; the others take what it begins with
+  RopeAxes axes;
+};
+
 constexpr int kRopeMaxWaves = 8;   // of a block, paired layout
 constexpr int kRopeWaves = 4;      // of a block, one chunk per lane
 
 enum RopeMode : int { ROPE_FORWARD = 0, ROPE_APPEND_ROWS = 1, ROPE_APPEND_MXFP4 = 2, ROPE_APPEND_MXFP8 = 3 };
 
-int launch_rope(int mode, int dtype, bool interleaved, const RopePlan& plan, const RopeArgs& args, void* stream,
+int launch_rope(int mode, int dtype, bool interleaved, const RopePlan& plan, const RopeAxesArgs& args, void* stream,
                 std::string* err);
 
 struct RopeGradSide {
@@ -130,9 +133,11 @@ struct RopeGradArgs {
   const float* cos_sin;
   int64_t ld_table, n_positions;
   const int64_t* positions;
-  RopeAxes axes;
   float inv_div, eps;
   float* partial;      // [rows][head_dim], see rope_grad_rows
+};
+struct RopeGradAxesArgs : RopeGradArgs {
+  RopeAxes axes;
 };
 
 constexpr int kGradWaves = 4;   // waves of a gradient block, each with tokens of its own
@@ -144,7 +149,7 @@ const void* rope_paired_grad_kernel(int dtype, bool interleaved, bool axes, cons
 // Rows of partial gamma gradients a launch writes.
 int64_t rope_grad_rows(const RopeGradArgs& a);
 
-int launch_rope_grad(int dtype, bool interleaved, const RopePlan& plan, const RopeGradArgs& args, void* stream,
+int launch_rope_grad(int dtype, bool interleaved, const RopePlan& plan, const RopeGradAxesArgs& args, void* stream,
                      std::string* err);
 
 struct AttendArgs {

@@ -206,7 +206,7 @@ Region gamma_region(const void* gamma, int64_t h, int64_t head_dim, int64_t gstr
 // ------------------------------------------------------------ forward, append
 struct RopeChecked {
   RopePlan plan;
-  RopeArgs args;
+  RopeAxesArgs args;
 };
 
 bool coded(const qknorm_cache_t* c) { return c->format != QKNORM_CACHE_ROWS; }
@@ -410,8 +410,8 @@ int check_rope(const char* fn, const qknorm_operand_t* q, const qknorm_operand_t
     return al.ok && table_aligned(rope, angles);
   });
   RopePlan& p = out->plan;
-  RopeArgs& a = out->args;
-  std::memset(&a, 0, sizeof a);
+  RopeAxesArgs& a = out->args;
+  a = RopeAxesArgs{};
   int slots_in[3] = {0, 0, 0};
   for (int c = 0; c < 3; ++c) {
     const qknorm_operand_t* o = ops[c];
@@ -499,7 +499,7 @@ size_t grad_workspace(int64_t heads_q, int64_t heads_k, int64_t T, int dtype, in
 
 int check_grad(const char* fn, const qknorm_grad_operand_t* q, const qknorm_grad_operand_t* k, int64_t T, int dtype,
                float eps, int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope, const qknorm_axes_t* axes,
-               void* ws, size_t ws_bytes, RopePlan* plan, RopeGradArgs* args, bool* noop) {
+               void* ws, size_t ws_bytes, RopePlan* plan, RopeGradAxesArgs* args, bool* noop) {
   *noop = false;
   if (!q || !k) return fail(QKNORM_ERR_INVALID_ARG, "%s: q and k operand descriptors are required", fn);
   int rc = check_common(fn, T, dtype, false, eps, head_dim, gstride, rope);
@@ -573,8 +573,8 @@ int check_grad(const char* fn, const qknorm_grad_operand_t* q, const qknorm_grad
     }
     return al.ok && table_aligned(rope, angles);
   });
-  RopeGradArgs& a = *args;
-  std::memset(&a, 0, sizeof a);
+  RopeGradAxesArgs& a = *args;
+  a = RopeGradAxesArgs{};
   for (int c = 0; c < 2; ++c) {
     const qknorm_grad_operand_t* o = ops[c];
     a.first[c] = a.n_slots;
@@ -725,7 +725,7 @@ int rope_backward(const char* fn, const qknorm_grad_operand_t* q, const qknorm_g
                   float eps, int64_t head_dim, int64_t gstride, const qknorm_rope_t* rope, const qknorm_axes_t* axes,
                   void* workspace, size_t workspace_bytes, void* stream) {
   RopePlan plan;
-  RopeGradArgs args;
+  RopeGradAxesArgs args;
   bool noop;
   const int rc = check_grad(fn, q, k, T, dtype, eps, head_dim, gstride, rope, axes, workspace, workspace_bytes, &plan,
                             &args, &noop);

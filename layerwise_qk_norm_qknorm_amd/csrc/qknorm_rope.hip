@@ -335,7 +335,7 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
 // 70 us. The paired layout is faster only for a cache of rows and about a
 // thousand tokens (10.7 us against 11.7).
 template <class IO, int S, bool INTER, int MODE, bool AXES>
-__global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeArgs a) {
+__global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const std::conditional_t<AXES, RopeAxesArgs, RopeArgs> a) {
   constexpr int VW = IO::kVW;
   constexpr bool CODES = MODE == ROPE_APPEND_MXFP4 || MODE == ROPE_APPEND_MXFP8;
   using MX = std::conditional_t<MODE == ROPE_APPEND_MXFP8, Mx8, Mx4>;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
   using T = Turn<IO, INTER, AXES>;
   __shared__ __align__(16) float angles[kRopeWaves * T::kLds];
   float* const lds = angles + (threadIdx.x >> 6) * T::kLds;
-  const uint32_t axes = AXES && turns ? lane_axes(a.axes) : 0;
+  const uint32_t axes = AXES && turns ? lane_axes(a) : 0;
 
   const char* gamma = static_cast<const char*>(c == 2 ? nullptr : o.gamma);
   Piece<GB> gam;   // of the first slot: of all where heads share it
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const RopeAr
 // bf16 columns: 59.5 us with the sums (56 and 5 traced one by one), 5.1 TB/s
 // where a copy of one stream reaches 6.06; 32 float32 heads 72.9 us, 5.6 TB/s.
 template <class IO, bool INTER, bool AXES>
-__global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGradArgs a) {
+__global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const std::conditional_t<AXES, RopeGradAxesArgs, RopeGradArgs> a) {
   constexpr int VW = IO::kVW;
   constexpr int GB = VW * IO::kGBytes;
   __shared__ float red[kGradWaves * 64 * VW];
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) qknorm_rope_grad(const RopeGr
   using T = Turn<IO, INTER, AXES>;
   __shared__ __align__(16) float angles[kGradWaves * T::kLds];
   float* const lds = angles + wave * T::kLds;
-  const uint32_t axes = AXES ? lane_axes(a.axes) : 0;
+  const uint32_t axes = lane_axes(a);
   const uint32_t off = (uint32_t)(hc * a.head_dim + at.col) * IO::kBytes;
 
   float g[VW], sum[VW];
@@ -698,7 +698,7 @@ int launched(hipError_t e, std::string* err) {
 
 constexpr int64_t kRopeMostBlocks = (int64_t)1 << 22;
 
-static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeArgs a, void* stream, std::string* err) {
+static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeAxesArgs a, void* stream, std::string* err) {
   const void* fn = rope_kernel(mode, dtype, inter, a.axes.n > 0, p);
   if (!fn) {
     *err = "no kernel compiled for this plan";
@@ -727,12 +727,12 @@ static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeA
                   err);
 }
 
-int launch_rope(int mode, int dtype, bool inter, const RopePlan& p, const RopeArgs& args, void* stream,
+int launch_rope(int mode, int dtype, bool inter, const RopePlan& p, const RopeAxesArgs& args, void* stream,
                 std::string* err) {
   if (!p.apart) return launch_rows(mode, dtype, inter, p, args, stream, err);
   // Q by itself, in the row-type kernel (it writes rows only), then K and V
   RopePlan part = p;
-  RopeArgs a = args;
+  RopeAxesArgs a = args;
   a.side[1].heads = a.side[2].heads = 0;
   a.first[2] = a.first[1];
   part.groups = a.first[1];
@@ -749,10 +749,10 @@ int64_t rope_grad_rows(const RopeGradArgs& a) {
   return (int64_t)(a.gstride == 0 ? a.n_slots : a.side[0].heads + a.side[1].heads) * a.workers;
 }
 
-int launch_rope_grad(int dtype, bool inter, const RopePlan& p, const RopeGradArgs& args, void* stream,
+int launch_rope_grad(int dtype, bool inter, const RopePlan& p, const RopeGradAxesArgs& args, void* stream,
                      std::string* err) {
   const void* fn = rope_grad_kernel(dtype, inter, args.axes.n > 0, p);
-  RopeGradArgs a = args;
+  RopeGradAxesArgs a = args;
   void* kargs[] = {&a};
   const int rc = launched(hipLaunchKernel(fn,
                                           dim3((unsigned)a.workers, (unsigned)a.n_slots), dim3(64 * kGradWaves), kargs,

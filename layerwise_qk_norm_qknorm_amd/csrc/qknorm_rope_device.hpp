@@ -229,8 +229,12 @@ struct AxisAngles {
     __builtin_amdgcn_wave_barrier();
   }
 };
-// The axes of a lane's held angles, two bits each.
-__device__ __forceinline__ uint32_t lane_axes(const RopeAxes& axes) {
+// The axes of a lane's held angles, two bits each (arguments without axes: none).
+__device__ __forceinline__ uint32_t lane_axes(const RopeArgs&) { return 0; }
+__device__ __forceinline__ uint32_t lane_axes(const RopeGradArgs&) { return 0; }
+template <class Args>
+__device__ __forceinline__ uint32_t lane_axes(const Args& a) {
+  const RopeAxes& axes = a.axes;
   uint32_t own = 0;
 #pragma unroll
   for (int r = 0; r < kHeldRounds; ++r) {

@@ -202,7 +202,7 @@ __device__ __forceinline__ void quantize_slot(const float* val, const RopeArgs& 
 // block's waves. All loads of a wave's slots are issued before the first is
 // used.
 template <class IO, int PB, int NP, int S, bool INTER, int MODE, bool AXES>
-__global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const RopeArgs a) {
+__global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const std::conditional_t<AXES, RopeAxesArgs, RopeArgs> a) {
   constexpr bool CODES = MODE == ROPE_APPEND_MXFP4 || MODE == ROPE_APPEND_MXFP8;
   using MX = std::conditional_t<MODE == ROPE_APPEND_MXFP8, Mx8, Mx4>;
   constexpr int VW = PB / IO::kBytes;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
   using Turns = Angles<VW, NP, INTER, AXES>;
   __shared__ __align__(16) float angles[kRopeMaxWaves * Turns::kLds];
   float* const lds = angles + wave * Turns::kLds;
-  const uint32_t axes = AXES ? lane_axes(a.axes) : 0;
+  const uint32_t axes = lane_axes(a);
 
   // What the wave's slots hold, the same for all its tokens: the side (Q, K or
   // V), the lane's byte offset in its rows, and gamma.
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(64 * kRopeMaxWaves) qknorm_rope_paired(const R
 // order, so the gradients do not change from run to run. The next token's
 // loads are issued before the current one is worked on.
 template <class IO, int PB, int NP, bool INTER, bool AXES>
-__global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(const RopeGradArgs a) {
+__global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(const std::conditional_t<AXES, RopeGradAxesArgs, RopeGradArgs> a) {
   constexpr int VW = PB / IO::kBytes;
   constexpr int GB = VW * IO::kGBytes;
   constexpr int E = 2 * NP * VW;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
   using Turns = Angles<VW, NP, INTER, AXES>;
   __shared__ __align__(16) float angles[kGradWaves * Turns::kLds];
   float* const lds = angles + wave * Turns::kLds;
-  const uint32_t axes = AXES ? lane_axes(a.axes) : 0;
+  const uint32_t axes = lane_axes(a);
 
   float gfa[NP][VW], gfb[NP][VW];
   float sa[NP][VW], sb[NP][VW];
@@ -557,22 +557,22 @@ __global__ void __launch_bounds__(64 * kGradWaves, 3) qknorm_rope_paired_grad(co
   }
 }
 
-using RopeFn = void (*)(const RopeArgs);
-using GradFn = void (*)(const RopeGradArgs);
+using RopeFn = const void*;      // kernels of two argument types
+using GradFn = const void*;
 
 template <class IO, bool INTER, int MODE, bool AXES>
 RopeFn pick_rope(const RopePlan& p) {
   if (p.piece_bytes == 16) {
     switch (p.slots) {
-      case 1: return qknorm_rope_paired<IO, 16, 1, 1, INTER, MODE, AXES>;
-      case 3: return qknorm_rope_paired<IO, 16, 1, 3, INTER, MODE, AXES>;
+      case 1: return reinterpret_cast<const void*>(qknorm_rope_paired<IO, 16, 1, 1, INTER, MODE, AXES>);
+      case 3: return reinterpret_cast<const void*>(qknorm_rope_paired<IO, 16, 1, 3, INTER, MODE, AXES>);
     }
     return nullptr;
   }
   if (p.slots != 1) return nullptr;
-  if (p.piece_bytes == 8) return qknorm_rope_paired<IO, 8, 1, 1, INTER, MODE, AXES>;
-  if (p.np == 1) return qknorm_rope_paired<IO, IO::kBytes, 1, 1, INTER, MODE, AXES>;
-  return qknorm_rope_paired<IO, IO::kBytes, 8, 1, INTER, MODE, AXES>;
+  if (p.piece_bytes == 8) return reinterpret_cast<const void*>(qknorm_rope_paired<IO, 8, 1, 1, INTER, MODE, AXES>);
+  if (p.np == 1) return reinterpret_cast<const void*>(qknorm_rope_paired<IO, IO::kBytes, 1, 1, INTER, MODE, AXES>);
+  return reinterpret_cast<const void*>(qknorm_rope_paired<IO, IO::kBytes, 8, 1, INTER, MODE, AXES>);
 }
 
 template <class IO, bool INTER, bool AXES>
@@ -594,10 +594,10 @@ RopeFn pick_rope_turn(int mode, bool inter, bool axes, const RopePlan& p) {
 
 template <class IO, bool INTER, bool AXES>
 GradFn pick_grad(const RopePlan& p) {
-  if (p.piece_bytes == 16) return qknorm_rope_paired_grad<IO, 16, 1, INTER, AXES>;
-  if (p.piece_bytes == 8) return qknorm_rope_paired_grad<IO, 8, 1, INTER, AXES>;
-  if (p.np == 1) return qknorm_rope_paired_grad<IO, IO::kBytes, 1, INTER, AXES>;
-  return qknorm_rope_paired_grad<IO, IO::kBytes, 8, INTER, AXES>;
+  if (p.piece_bytes == 16) return reinterpret_cast<const void*>(qknorm_rope_paired_grad<IO, 16, 1, INTER, AXES>);
+  if (p.piece_bytes == 8) return reinterpret_cast<const void*>(qknorm_rope_paired_grad<IO, 8, 1, INTER, AXES>);
+  if (p.np == 1) return reinterpret_cast<const void*>(qknorm_rope_paired_grad<IO, IO::kBytes, 1, INTER, AXES>);
+  return reinterpret_cast<const void*>(qknorm_rope_paired_grad<IO, IO::kBytes, 8, INTER, AXES>);
 }
 
 template <class IO>
@@ -609,14 +609,13 @@ GradFn pick_grad_turn(bool inter, bool axes, const RopePlan& p) {
 }  // namespace
 
 const void* rope_paired_kernel(int mode, int dtype, bool inter, bool axes, const RopePlan& p) {
-  return reinterpret_cast<const void*>(dtype == kDtypeBF16  ? pick_rope_turn<BF16>(mode, inter, axes, p)
-                                       : dtype == kDtypeF32 ? pick_rope_turn<F32>(mode, inter, axes, p)
-                                                            : pick_rope_turn<FP8>(mode, inter, axes, p));
+  return dtype == kDtypeBF16  ? pick_rope_turn<BF16>(mode, inter, axes, p)
+         : dtype == kDtypeF32 ? pick_rope_turn<F32>(mode, inter, axes, p)
+                              : pick_rope_turn<FP8>(mode, inter, axes, p);
 }
 
 const void* rope_paired_grad_kernel(int dtype, bool inter, bool axes, const RopePlan& p) {
-  return reinterpret_cast<const void*>(dtype == kDtypeBF16 ? pick_grad_turn<BF16>(inter, axes, p)
-                                                           : pick_grad_turn<F32>(inter, axes, p));
+  return dtype == kDtypeBF16 ? pick_grad_turn<BF16>(inter, axes, p) : pick_grad_turn<F32>(inter, axes, p);
 }
 
 }  // namespace qkn

@@ -59,8 +59,7 @@ struct Call {
 
   int run(void* stream) const {
     const qknorm_rope_t* r = has_rope ? &rope : nullptr;
-    qknorm_axes_t ax = axes;
-    ax.axis = reinterpret_cast<const uint8_t*>(axis.data());
+    const qknorm_axes_t ax{axes.n_axes, reinterpret_cast<const uint8_t*>(axis.data()), axes.ld_positions};
     switch (kind) {
       case ROPE:
         if (has_axes) return qknorm_headwise_rope_axes(&q, &k, T, dtype, eps, head_dim, gstride, r, &ax, stream);
