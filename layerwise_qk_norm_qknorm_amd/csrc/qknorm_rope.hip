@@ -192,47 +192,55 @@ struct Coded {
   int byte;
 };
 
+// The largest magnitude of a lane's values, NaN where one of them is.
+template <int VW>
+__device__ __forceinline__ float largest(const float (&f)[VW]) {
+  float m = __builtin_fabsf(f[0]);
+#pragma unroll
+  for (int e = 1; e < VW; e += 2)
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(f[e])),
+                                      __builtin_fabsf(f[(e + 1) % VW]));
+  return m;
+}
+
 // The codes of a lane's values.
 template <class MX, int VW>
 __device__ __forceinline__ Coded<MX, VW> quantize(const float (&f)[VW]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < VW; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
   Coded<MX, VW> q;
-  q.byte = scale_byte<MX>(block_max<VW>(m));
+  q.byte = scale_byte<MX>(block_max<VW>(__float_as_uint(largest(f)) & 0x7FFFFFFFu));
   const float inv = over_scale(q.byte);
   float a[VW];
 #pragma unroll
-  for (int e = 0; e < VW; ++e) a[e] = q.byte == 0xFF ? 0.0f : f[e] * inv;
+  for (int e = 0; e < VW; ++e) a[e] = MX::saturated(f[e] * inv);
+  if (__builtin_amdgcn_ballot_w64(q.byte == 0xFF) != 0) {
+    keep_branch();
+#pragma unroll
+    for (int e = 0; e < VW; ++e) a[e] = q.byte == 0xFF ? 0.0f : a[e];
+  }
   q.codes = codes_of<MX, VW>(a);
   return q;
 }
 
 // The codes of values known to within kUnsure of `mag`: true if every value
-// within that distance has them (in this lane's share of its block).
-constexpr float kUnsure = 0x1p-19f;
+// within that distance has them (in this lane's share of its block). A value and
+// both ends of its interval are of one sign, or their codes differ; 0 is its own
+// interval where mag is 0.
+constexpr float kUnsure = 0x1.4p-20f;
 template <class MX, int VW>
 __device__ __forceinline__ bool quantize_sure(const float (&f)[VW], const float (&mag)[VW], Coded<MX, VW>& q) {
-  float lo[VW], hi[VW];
-  uint32_t ml = 0, mh = 0;
-#pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    const float v = __builtin_fabsf(f[e]);
-    hi[e] = __builtin_fmaf(mag[e], kUnsure, v);
-    lo[e] = __builtin_fmaf(mag[e], -kUnsure, v);
-    lo[e] = lo[e] > 0.0f ? lo[e] : 0.0f;        // NaN: 0, which differs from hi's
-    ml = max(ml, __float_as_uint(lo[e]));
-    mh = max(mh, __float_as_uint(hi[e]) & 0x7FFFFFFFu);
-  }
-  ml = block_max<VW>(ml);
-  mh = block_max<VW>(mh);
+  const float top = __uint_as_float(block_max<VW>(__float_as_uint(largest(f)) & 0x7FFFFFFFu));
+  const float far = __uint_as_float(block_max<VW>(__float_as_uint(largest(mag)) & 0x7FFFFFFFu));
+  const float most = __builtin_fmaf(far, kUnsure, top), least = __builtin_fmaf(far, -kUnsure, top);
+  const uint32_t mh = __float_as_uint(most) & 0x7FFFFFFFu;
   q.byte = scale_byte<MX>(mh);
-  if (mh >= 0x7F800000u || scale_byte<MX>(ml) != q.byte) return false;
-  const float inv = over_scale(q.byte);
+  if (mh >= 0x7F800000u || scale_byte<MX>(least > 0.0f ? __float_as_uint(least) : 0u) != q.byte) return false;
+  const float inv = over_scale(q.byte), width = kUnsure * inv;
+  float lo[VW], hi[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    hi[e] = __builtin_copysignf(hi[e] * inv, f[e]);
-    lo[e] = __builtin_copysignf(lo[e] * inv, f[e]);
+    const float v = MX::saturated(f[e] * inv), w = mag[e] * width;
+    hi[e] = v + w;
+    lo[e] = v - w;
   }
   q.codes = codes_of<MX, VW>(hi);
   return q.codes == codes_of<MX, VW>(lo);
@@ -263,7 +271,12 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
 #pragma unroll
     for (int e = 0; e < VW; ++e) ss = __builtin_fma((double)v[e], (double)v[e], ss);
     ss = group_sum_d(ss, L);
-    r = 1.0 / __builtin_sqrt(ss / a.head_dim + (double)a.eps);
+    // (head_dim is a power of two in this layout.) The hardware's estimate and two Newton
+    // steps instead of a division and a square root, which take 60 instructions more
+    const double m = __builtin_fma(ss, (double)a.inv_div, (double)a.eps);
+    r = __builtin_amdgcn_rsq(m);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) r = __builtin_fma(r * 0.5, __builtin_fma(-m * r, r, 1.0), r);
   }
   bool in = false;
   const float* row = nullptr;
@@ -464,16 +477,17 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const std::c
     }
 
     if constexpr (CODES) {
-      // A key's float32 value is within 16 u of the magnitudes it is the sum
-      // of (r within 11 u: a chain of 8 squares, 6 butterfly adds, the factor;
-      // then 4 roundings), u = 2^-24; kUnsure is twice that. It is so where the
-      // sum is finite (r > 0) and subnormal roundings, of 2^-150 at most, count
-      // for nothing: with r up to 2^24 they are below u of the mean square, and
-      // below kUnsure / 16 of the lowest border there is, 2^-102 (8 bits: 2^16 and
-      // 2^-110). Where a border of the codes or of the scale lies that near to one (in 2 or 3% of the
-      // slots), or r is out of that range, the slot is formed again in float64,
-      // so that every code is the one exact arithmetic gives and does not hang
-      // on the order of a sum.
+      // A key's float32 value is within 16 u of the magnitudes it is the sum of (r
+      // within 11 u: a chain of 8 squares, 6 butterfly adds, the factor; then 4
+      // roundings), u = 2^-24. kUnsure is 20 u: one more for the rounding of the
+      // interval's ends, and 3 u of the lowest border there is, 2^-102 (8 bits:
+      // 2^-110), are more than what subnormal roundings of 2^-150 come to where r is
+      // at most 2^24 (2^16): 2^-126 for each of the two that make a value. (Twice as
+      // wide, 8 bits take 1 us longer.) It is so where the sum is finite (r > 0).
+      // Where a border of the codes or of the scale lies that near to one (in 2% of
+      // the slots, with 8 bits in 5%), or r is out of that range, the slot is formed
+      // again in float64, so that every code is the one exact arithmetic gives and
+      // does not hang on the order of a sum.
       // Here, behind the others, where little else is held in registers (in
       // float64 throughout, 8192 tokens took 69 us).
 #pragma unroll 1

@@ -252,10 +252,13 @@ __device__ __forceinline__ uint32_t lane_axes(const Args& a) {
 struct Mx4 {   // E2M1
   static constexpr int kBits = 4, kLead = 2, kTop = 252;
   static constexpr float kMostFactor = 0x1p24f;
+  __device__ __forceinline__ static float saturated(float v) { return v; }   // by the conversion
 };
 struct Mx8 {   // E4M3
   static constexpr int kBits = 8, kLead = 8, kTop = 246;
   static constexpr float kMostFactor = 0x1p16f;
+  // the conversion makes NaN of what it would round to more than 448
+  __device__ __forceinline__ static float saturated(float v) { return __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f); }
 };
 
 // The scale byte of a block whose largest magnitude has these bits (NaN above infinity).
@@ -276,7 +279,8 @@ struct Codes {
     return same;
   }
 };
-// The codes of values already over the scale.
+// The codes of values already over the scale and saturated (as MX::saturated, or less than
+// half a step past the largest code).
 template <class MX, int VW>
 __device__ __forceinline__ Codes<MX, VW> codes_of(const float (&a)[VW]) {
   Codes<MX, VW> q;
@@ -290,11 +294,8 @@ __device__ __forceinline__ Codes<MX, VW> codes_of(const float (&a)[VW]) {
     }
     q.w[0] = w;
   } else {
-    float v[VW];   // finite: scaled values are below 512, and a block with others has none
 #pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = __builtin_amdgcn_fmed3f(a[e], -448.0f, 448.0f);
-#pragma unroll
-    for (int p = 0; p < VW / 4; ++p) q.w[p] = pack_fp8_word(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+    for (int p = 0; p < VW / 4; ++p) q.w[p] = pack_fp8_word(a[4 * p], a[4 * p + 1], a[4 * p + 2], a[4 * p + 3]);
   }
   return q;
 }

@@ -170,7 +170,7 @@ __device__ __forceinline__ void quantize_slot(const float* val, const RopeArgs& 
     const int byte = scale_byte<MX>(m);
     const float inv = over_scale(byte);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = byte == 0xFF ? 0.0f : f[e] * inv;
+    for (int e = 0; e < 8; ++e) f[e] = byte == 0xFF ? 0.0f : MX::saturated(f[e] * inv);
     const Codes<MX, 8> w = codes_of<MX, 8>(f);
     if (on) {
       store_bytes<MX::kBits>(codes + (int64_t)(head0 + h) * a.head_stride + c * MX::kBits / 8, w.w);
