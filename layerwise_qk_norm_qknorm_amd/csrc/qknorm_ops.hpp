@@ -184,7 +184,7 @@ struct AttendArgs {
 
 struct AttendPlan {
   int head_dim = 0;
-  int row_tile = 1;      // 16-row tiles per block: 1, 2 or 4
+  int row_tile = 1;      // 16-row tiles per block: 1, 2 or 4; wide caches 1, 2, 8 or 16
   int row_tiles = 1;
   int splits = 1;
   int most_splits = 1;   // what the workspace is sized for: no smaller for a longer max_len
@@ -198,7 +198,7 @@ int launch_attend(const AttendPlan& plan, const AttendArgs& args, void* stream, 
 int launch_attend_join(const AttendPlan& plan, const AttendArgs& args, void* stream, std::string* err);
 
 // Caches of bf16 rows and MXFP8 (mx8). row_tile 1 and 2: the kernel whose waves
-// share a block's rows; 8 and 16: the one whose waves take 32 and 64 rows each.
+// share a block's rows; 8 and 16: the one whose four or eight waves take 32 each.
 int launch_attend_wide(bool mx8, const AttendPlan& plan, const AttendArgs& args, void* stream, std::string* err);
 
 struct GatherArgs {

@@ -636,6 +636,28 @@ int64_t row_tiles_of(int64_t tiles, int64_t tile, int64_t heads_k, int64_t group
   const int64_t most = std::max(std::min(fill, kLaunchThreads / 256 / pairs), even);
   return std::min({tiles, most, (int64_t)65536});
 }
+//
+// parts_per_step: bytes of partial results that are written and read again in the
+// time of a step (0: not counted).
+void split_cache(AttendPlan* p, int64_t blocks, int64_t resident, int64_t group, int64_t max_len, int64_t window,
+                 int64_t part_bytes, int64_t parts_per_step) {
+  const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
+  p->most_splits = (int)most(max_len);
+  // what a block's rows see together, at most
+  const int64_t span = window && window < max_len ? std::min(max_len, window + 16 * p->row_tile / group + 33) : max_len;
+  const int64_t m = most(span);
+  int64_t least = INT64_MAX;
+  for (int64_t rounds = 0; rounds <= kRounds; ++rounds) {
+    const int64_t s = std::clamp<int64_t>(rounds * resident / blocks, 1, m);
+    int64_t chunk = ((span + s - 1) / s + 127) / 128 * 128;
+    if (chunk < 256) chunk = 256;
+    const int64_t n = (span + chunk - 1) / chunk;
+    int64_t cost = (blocks * n + resident - 1) / resident * (chunk / 128 + kBlockSteps);
+    if (n > 1) cost += kJoinSteps + (parts_per_step ? (int64_t)((double)n * (double)part_bytes / (double)parts_per_step) : 0);
+    if (cost < least) least = cost, p->splits = (int)n, p->chunk = (int)chunk;
+  }
+}
+
 AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t T, int64_t max_q,
                        int64_t max_len, int64_t window) {
   AttendPlan p;
@@ -646,27 +668,21 @@ AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t
   const int64_t resident = 256 * (p.row_tile * head_dim <= 128 ? 3 : 2);
   p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);
   p.max_q = max_q;
-  const int64_t blocks = B * heads_k * p.row_tiles;
-  const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
-  p.most_splits = (int)most(max_len);
-  // what a block's rows see together, at most
-  const int64_t span = window && window < max_len ? std::min(max_len, window + 16 * p.row_tile / group + 33) : max_len;
-  const int64_t m = most(span);
-  int64_t least = INT64_MAX;
-  for (int64_t rounds = 0; rounds <= kRounds; ++rounds) {
-    const int64_t s = std::clamp<int64_t>(rounds * resident / blocks, 1, m);
-    int64_t chunk = ((span + s - 1) / s + 127) / 128 * 128;
-    if (chunk < 256) chunk = 256;
-    const int64_t n = (span + chunk - 1) / chunk;
-    const int64_t cost = (blocks * n + resident - 1) / resident * (chunk / 128 + kBlockSteps) + (n > 1 ? kJoinSteps : 0);
-    if (cost < least) least = cost, p.splits = (int)n, p.chunk = (int)chunk;
-  }
+  split_cache(&p, B * heads_k * p.row_tiles, resident, group, max_len, window, 0, 0);
   return p;
 }
 
-// The same for caches of rows and MXFP8: up to 32 rows of a sequence share a block's
-// waves, beyond them each wave takes 32 rows of its own, and 64 from 129 rows on
-// (at 256 columns a wave's accumulators hold 32).
+// The same for caches of rows and MXFP8. Up to 32 rows of a sequence (of a key head)
+// share a block's four waves, which take the cache's tokens in turn; beyond them
+// each wave takes 32 rows, four waves to a block, and eight from 129 rows on at 128
+// columns, so that a staged tile serves 256 rows (4 x 531 .. 1024 rows x 5 heads on
+// 4215 .. 8192 tokens: 422 us with four, 371 with eight; at 64 columns four waves at
+// three blocks a unit are faster, 208 us against 213, at 256 their registers do not
+// suffice).
+//
+// A step of the latter takes 4.6 us, in which 18 MB of partial results go to memory
+// and back: 1024 rows x 5 heads on 4096 tokens, 160 blocks, are 123 us unsplit and
+// 144 in three parts.
 AttendPlan plan_attend_wide(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t T, int64_t max_q,
                             int64_t max_len, int64_t window) {
   AttendPlan p;
@@ -674,24 +690,11 @@ AttendPlan plan_attend_wide(int64_t head_dim, int64_t heads_k, int64_t group, in
   const int64_t rows = max_q * group;
   p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 128 || head_dim != 128 ? 8 : 16;
   const int64_t tiles = (rows + 16 * p.row_tile - 1) / (16 * p.row_tile);
-  const int64_t resident = 256 * (head_dim == 256 || p.row_tile == 16 ? 1 : 2);
+  const int64_t resident = 256 * (head_dim == 256 || p.row_tile == 16 ? 1 : head_dim == 64 && p.row_tile == 8 ? 3 : 2);
   p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);
   p.max_q = max_q;
-  const int64_t blocks = B * heads_k * p.row_tiles;
-  const auto most = [&](int64_t len) { return std::max<int64_t>(1, std::min((len + 255) / 256, kRounds * resident / blocks)); };
-  p.most_splits = (int)most(max_len);
-  // what a block's rows see together, at most
-  const int64_t span = window && window < max_len ? std::min(max_len, window + 16 * p.row_tile / group + 33) : max_len;
-  const int64_t m = most(span);
-  int64_t least = INT64_MAX;
-  for (int64_t rounds = 0; rounds <= kRounds; ++rounds) {
-    const int64_t s = std::clamp<int64_t>(rounds * resident / blocks, 1, m);
-    int64_t chunk = ((span + s - 1) / s + 127) / 128 * 128;
-    if (chunk < 256) chunk = 256;
-    const int64_t n = (span + chunk - 1) / chunk;
-    const int64_t cost = (blocks * n + resident - 1) / resident * (chunk / 128 + kBlockSteps) + (n > 1 ? kJoinSteps : 0);
-    if (cost < least) least = cost, p.splits = (int)n, p.chunk = (int)chunk;
-  }
+  split_cache(&p, B * heads_k * p.row_tiles, resident, group, max_len, window, T * heads_k * group * (head_dim + 2) * 8,
+              p.row_tile >= 8 ? 18 * 1000 * 1000 : 0);
   return p;
 }
 

@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(64 * kRopeWaves) qknorm_rope_rows(const std::c
       // 2^-110), are more than what subnormal roundings of 2^-150 come to where r is
       // at most 2^24 (2^16): 2^-126 for each of the two that make a value. (Twice as
       // wide, 8 bits take 1 us longer.) It is so where the sum is finite (r > 0).
-      // Where a border of the codes or of the scale lies that near to one (in 2% of
-      // the slots, with 8 bits in 5%), or r is out of that range, the slot is formed
+      // Where a border of the codes or of the scale lies that near to one (in 0.4% of
+      // the slots, with 8 bits in 6%), or r is out of that range, the slot is formed
       // again in float64, so that every code is the one exact arithmetic gives and
       // does not hang on the order of a sum.
       // Here, behind the others, where little else is held in registers (in
