@@ -216,10 +216,10 @@ struct GatherArgs {
   int groups;              // waves of 64 items that a token's heads take
   Divisor by_pieces, by_groups;
   uint32_t units;          // waves of the launch
-  int64_t tokens;          // that these cover; the rest loop
+  int64_t tokens;          // runs of tokens that these cover; the rest loop
 };
 enum GatherKind : int { GATHER_ROWS = 0, GATHER_MXFP4 = 1, GATHER_MXFP8 = 2 };
-// piece_bytes: of the rows written, 16 (MX formats: eight elements in 16-byte stores) or one element.
+// piece_bytes: of the rows' loads and stores, 16 or one element (codes: of the stores; a piece is 16 bytes of rows).
 int launch_gather(int kind, int dtype, int piece_bytes, const GatherArgs& args, void* stream, std::string* err);
 
 }  // namespace qkn

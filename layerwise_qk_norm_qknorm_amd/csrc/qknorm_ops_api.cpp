@@ -824,7 +824,7 @@ int gather(const char* fn, const qknorm_cache_t* cache, int64_t head_dim, const 
   a.n_tokens_held = cache->n_pages * cache->page_size;
   a.log2_page = log2_of(cache->page_size);
   a.head_dim = (int)head_dim;
-  a.pieces = (int)(codes ? head_dim / 8 : head_dim * esz / piece_bytes);
+  a.pieces = (int)(head_dim * esz / (codes ? 16 : piece_bytes));
   a.items = (int)(cache->heads * a.pieces);
   a.groups = (a.items + 63) / 64 * (k_rows && v_rows ? 2 : 1);
   const int kind = cache->format == QKNORM_CACHE_ROWS    ? GATHER_ROWS
