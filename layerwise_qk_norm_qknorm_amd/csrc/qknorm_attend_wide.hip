@@ -756,8 +756,8 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
             for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
           const char* kp = kbuf + cur * kTileK + m * LDK + g * 16;
           // reads of K ahead of the products that take them, which the compiler would
-          // otherwise wait for two by two
-          constexpr int kAhead = D == 64 ? 4 : 6;
+          // otherwise wait for two by two (two, three, six or eight ahead measure the same)
+          constexpr int kAhead = 4;
           Frag kf[TB * KS];
           const auto read_k = [&](int i) {
             const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kp + 32 * (i % TB) * LDK + 32 * (i / TB));
@@ -801,9 +801,24 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) acc[mb] *= alpha;
           }
+          // This product goes before the other waves of its SIMD, whose exponentials and
+          // conversions fill in between: 390 us at equal priority, 383 so, for 8192 tokens of
+          // 32 heads on 8 of 128 channels, 16384 cached (381 and 373 with rows of MXFP8; the
+          // first product's priority makes no difference)
+          __builtin_amdgcn_s_setprio(1);
           // out += V^T P^T. A transposing read gives 16 lanes four tokens of 16 channels: lane
           // (m, g) holds tokens 4g .. 4g + 3 and 8 + 4g .. of channel m, as it holds of P
           const char* vp = vbuf + cur * kTileV + (4 * g + ((lane & 15) >> 2)) * LDV + (16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
+          // two reads ahead of the products and of the exponentials before them: heads of 256
+          // take 483 us instead of 557, others 1 % less; four ahead, 503
+          constexpr int kAheadV = 2;
+          Frag vf[2 * TB * MB];
+          const auto read_v = [&](int n) {
+            const char* p = vp + 16 * (n / MB) * LDV + 64 * (n % MB);
+            vf[n] = join4(read_transposed(p), read_transposed(p + 8 * LDV));
+          };
+#pragma unroll
+          for (int n = 0; n < kAheadV; ++n) read_v(n);
 #pragma unroll
           for (int ks = 0; ks < 2 * TB; ++ks) {
             Frag pf;
@@ -817,11 +832,12 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
             }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-              const char* p = vp + 16 * ks * LDV + 64 * mb;
-              const Frag vf = join4(read_transposed(p), read_transposed(p + 8 * LDV));
-              acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.get(), pf.get(), acc[mb], 0, 0, 0);
+              const int n = ks * MB + mb;
+              if (n + kAheadV < 2 * TB * MB) read_v(n + kAheadV);
+              acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n].get(), pf.get(), acc[mb], 0, 0, 0);
             }
           }
+          __builtin_amdgcn_s_setprio(0);
         }
         if (more) store(tok + kTok, cur ^ 1);
         __syncthreads();
