@@ -901,7 +901,8 @@ int attend(const char* fn, bool wide, const qknorm_operand_t* q, int64_t T, int 
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
   AttendPlan p = (wide ? plan_attend_wide : plan_attend)(head_dim, cache->heads, heads_q / cache->heads, batch->B, T,
                                                          max_q, max_len, window);
-  if ((int64_t)batch->B * cache->heads * p.row_tiles > kLaunchThreads / 256 / p.splits)
+  const int64_t block = wide && p.row_tile == 16 ? 512 : 256;
+  if ((int64_t)batch->B * cache->heads * p.row_tiles > kLaunchThreads / block / p.splits)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the launch exceeds the grid", fn);
   const size_t need = attend_workspace(p, T, heads_q);
   if (need && (!workspace || !multiple(workspace, 16) || workspace_bytes < need))
