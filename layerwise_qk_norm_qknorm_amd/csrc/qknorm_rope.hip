@@ -733,6 +733,19 @@ static int launch_rows(int mode, int dtype, bool inter, const RopePlan& p, RopeA
     // gy blocks take a token's slots: the cap holds for their product, down to one token's blocks
     gy = (unsigned)((a.n_slots + p.slots * p.waves - 1) / (p.slots * p.waves));
     const int64_t most = (grid_cap() < kRopeMostBlocks ? grid_cap() : kRopeMostBlocks) / gy;
+    // Of bf16 rows a compute unit holds eight waves of three slots. Where there are more,
+    // these take several tokens each, in equal numbers, and load the next one's rows before
+    // this one's work: 8192 tokens of 32 + 8 heads of 80 on three axes 29.5 us, a wave a
+    // token 37.3; heads of 96 34.2 and 39.5, and appended to MXFP8 with one position 51.9
+    // and 62.3. Not codes with several axes, whose registers do not suffice for two tokens
+    // (74 us, 63.3), nor rows with several axes (41 either way); calls with one position and
+    // no MXFP8 keep a wave a token.
+    const bool shared = (mode == ROPE_FORWARD && a.axes.n > 0) || (mode == ROPE_APPEND_MXFP8 && a.axes.n == 0);
+    const int64_t held = 256 * 8 / ((int64_t)p.waves * p.tokens * gy);
+    if (shared && dtype == kDtypeBF16 && p.slots == 3 && held > 0 && blocks > held) {
+      const int64_t rounds = (blocks + held - 1) / held;
+      blocks = (blocks + rounds - 1) / rounds;
+    }
     if (blocks > most) blocks = most > 0 ? most : 1;
   }
   void* kargs[] = {&a};

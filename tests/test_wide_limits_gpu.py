@@ -159,3 +159,39 @@ def test_rows_read_back_past_32_bits():
     for t, s in enumerate(slots.tolist()):
         want = cache[0][s // ps, :, s % ps].reshape(-1) if s >= 0 else torch.full((heads * d,), 3.0, device="cuda").bfloat16()
         assert C.same_bits(far[t], want), t
+
+
+@pytest.mark.parametrize("T", [2049, 9001])
+@pytest.mark.parametrize("d", [80, 96, 192])
+def test_waves_of_several_tokens(d, T):
+    """More tokens than the chip holds waves of: the bits of calls of 300 tokens, which it does hold."""
+    hq, hk, ps = 24, 5, 16
+    r = C.rng(T)
+    x = torch.randn((T, (hq + 2 * hk) * d), generator=torch.Generator(device="cuda").manual_seed(d), device="cuda").bfloat16()
+    q, k, v = x.split([hq * d, hk * d, hk * d], 1)
+    gamma = [torch.from_numpy(r.normal(1, 0.2, d)).bfloat16().cuda() for _ in range(2)]
+    td, pos = C.dev(C.table(512, d)), C.dev(r.integers(0, 512, (3, T)))
+    names = qk.rope_axes((d // 2 - 20, 10, 10))
+    slots = C.dev(r.permutation(T + 50)[:T].astype(np.int64))
+    pages = -(-(T + 50) // ps)
+
+    def run(step):
+        oq, ok = torch.empty((T, hq * d), dtype=x.dtype, device="cuda"), torch.empty((T, hk * d), dtype=x.dtype, device="cuda")
+        out = [oq, ok]
+        for t in range(0, T, step):
+            s = slice(t, min(T, t + step))
+            qk.qknorm_headwise_rope_axes(q[s], k[s], *gamma, EPS, d, td, pos[:, s], names, out_q=oq[s], out_k=ok[s])
+        if d % 32 == 0:
+            cache = [torch.zeros((pages, hk, ps, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+            scales = [torch.zeros((pages, hk, ps, d // 32), dtype=torch.uint8, device="cuda") for _ in range(2)]
+            aq = torch.empty_like(oq)
+            for t in range(0, T, step):
+                s = slice(t, min(T, t + step))
+                qk.qknorm_paged_append(q[s], k[s], v[s], *gamma, EPS, d, td, pos[0, s], *cache, slots[s], *scales,
+                                       out_q=aq[s])
+            out += cache + scales + [aq]
+        torch.cuda.synchronize()
+        return out
+
+    for a, b in zip(run(T), run(300)):
+        assert C.same_bits(a, b)
