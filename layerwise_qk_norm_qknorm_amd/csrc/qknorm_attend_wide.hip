@@ -7,8 +7,9 @@
 // when m grows. MXFP8 codes are widened to bf16 with their scale applied,
 // exactly (four significant bits times a power of two), so both products run on
 // bf16 MFMA tiles with nothing lost on the K and V side. Probabilities are
-// rounded to bf16 (at most half a step, 2^-8 relative, averaged over the tokens); scores, m, l and the accumulator are float32, and l sums the rounded
-// probabilities.
+// rounded to bf16, which the second product takes (at most half a step, 2^-8
+// relative, averaged over the tokens); scores, m, l and the accumulator are
+// float32, and l sums the rounded probabilities.
 //
 // Scores are formed transposed (tokens x rows), so that a lane holds one row's
 // scores, and those are the positions it must hold of the second product's
@@ -17,10 +18,22 @@
 //
 // Two kernels. qknorm_attend_few, for up to 32 rows of a sequence and key head:
 // the four waves of a block take the 32-token tiles of its part of the cache in
-// turn, K straight into registers, and join in LDS at the end; bound by the
-// cache's bytes. qknorm_attend_many, beyond: each wave takes 32 rows of its own, and
-// all share K and V tiles of 64 tokens that the block stages in LDS;
-// bound by the matrix and the vector unit.
+// turn, K straight into registers, and join in LDS at the end. Bound by the
+// cache's bytes: 64 single tokens of 40 over 8 heads of 128 on up to 8192 take 278 us
+// from rows, 5.6 TB/s, and 153 from MXFP8, 5.3; one on 65536 in MXFP8 25 us and
+// 5 us of joining its splits. Tiles of 32 tokens, since a wave's K and V in flight
+// then fill its registers at two blocks a compute unit; two tiles in flight, and
+// eight waves, were no faster.
+//
+// qknorm_attend_many, beyond: each wave takes 32 rows of its own, and all share K
+// and V tiles of 64 tokens that the block stages in LDS, the next one loaded into
+// registers behind the products. A wave of 32 rows reads each staged byte once for
+// 32 x 32 x 16 products, half of what 16 rows would take of LDS; 64 tokens, so that
+// two independent chains of products hide each other's latency. 4 x 531 .. 1024 rows
+// of those heads on 4215 .. 8192 cached tokens: 370 us, 980 TFLOP/s (an 8192^3 library
+// product reaches 1184), MXFP8 360. The matrix unit is busy 48 % and the vector unit,
+// with the exponentials, roundings and maxima, 41 % of the time; without the loads it
+// would take 337 us, without the exponentials 343.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -532,7 +545,9 @@ __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) qknorm_attend_f
 // the chip holds at once, so the longest go first: up to 64 sequences by their
 // cached tokens, each one's last rows first, and blocks for rows that a sequence
 // does not have come last of all. 4 x 531 .. 1024 rows on 4215 .. 8192 tokens, 40
-// over 8 heads of 128: in the order of the sequences 680 us, so ordered 540.
+// over 8 heads of 128, four waves a block: in the order of the sequences 680 us, so
+// ordered and with both halves of a tile in flight 432; the order alone takes a
+// simulated schedule from 1.37 to 1.04 of the mean load.
 // Consecutive blocks take the key heads in turn: where they divide by 8, a head's
 // blocks run on one XCD, whose L2 then holds its cache.
 struct Work {

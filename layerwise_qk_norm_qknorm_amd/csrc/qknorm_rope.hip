@@ -20,6 +20,8 @@
 // needs no exchange but reads a head in two 128-byte runs per instruction.
 // 8192 tokens x 48 heads x 128 bf16 columns: half-split 39.0 -> 36.6 us (5.6
 // TB/s; float32 71.5, 5.7 TB/s; FP8 35.7, bound by its conversions), interleaved 45 -> 36.6, no rotation 43 -> 36; gradients 79 -> 59.
+// Positions on three axes add the gathering of the token's angles by each wave (351
+// vector instructions a wave, 275 with one position): 38.7 us and, gradients, 60.8.
 // Slots never mix Q, K and V, so all that depends on the side is scalar. Other
 // heads take the layout of qknorm_rope_paired.hip.
 
@@ -343,7 +345,9 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
 // 8192 tokens of 40 + 8 + 8 bf16 heads of 128 into a 4-bit cache: 60.4 us, 4.1
 // TB/s, 58.1 without the cached values as rows; Q's launch 33 us runs at 5.1
 // TB/s, K's and V's 27 us is bound by the quantisation (504 vector instructions
-// a wave, 65% of the cycles). Into a cache of bf16 rows 42.0 us, 5.7 TB/s.
+// a wave, 65% of the cycles). Into a cache of bf16 rows 42.0 us, 5.7 TB/s. Into an
+// 8-bit cache, on three axes, 67.2: Q's launch 37 us, K's and V's 30 (564 vector
+// instructions a wave).
 // Apart, because one kernel for both took the registers of the longer one:
 // 70 us. The paired layout is faster only for a cache of rows and about a
 // thousand tokens (10.7 us against 11.7).

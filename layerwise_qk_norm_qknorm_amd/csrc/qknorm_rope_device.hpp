@@ -145,8 +145,9 @@ __device__ __forceinline__ void narrow(const float (&v)[VW], uint32_t* w) {
 // (lane + 64 r), from the rows that their axes' positions name, and lays them side
 // by side in LDS, where its lanes then read them as they would a row of the table:
 // two loads of 4 bytes a lane instead of its chunk's angles for each lane, whatever
-// the order of the axes (8192 tokens of 40 + 8 bf16 heads of 128: sections 43.2 ->
-// AXES_S us, axes in turn 63 -> AXES_T; a single position, loaded as chunks, 37.0).
+// the order of the axes (8192 tokens of 40 + 8 bf16 heads of 128: sections 43.2 us
+// with each lane's own loads, 38.7 so; axes in turn 63 and 39.4; a single position,
+// loaded as chunks, 36.6).
 // Angles past the first 128 are gathered when they are laid down, so that they
 // take no registers (rotations of more than 256 columns).
 constexpr int kSinAt(int rounds) { return 64 * rounds; }     // floats; rounds: 64 angles each
