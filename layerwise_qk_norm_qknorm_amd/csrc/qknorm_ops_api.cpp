@@ -678,7 +678,9 @@ AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t
 // columns, so that a staged tile serves 256 rows (4 x 531 .. 1024 rows x 5 heads on
 // 4215 .. 8192 tokens: 422 us with four, 371 with eight; at 64 columns four waves at
 // three blocks a unit are faster, 208 us against 213, at 256 their registers do not
-// suffice).
+// suffice). 257 to 384 rows take four again, which leave no third of the blocks'
+// rows empty (4 x up to 64 rows x 5 heads on those tokens 78 us against 90; from 385
+// on eight are as fast or faster).
 //
 // A step of the latter takes 4.6 us, in which 18 MB of partial results go to memory
 // and back: 1024 rows x 5 heads on 4096 tokens, 160 blocks, are 123 us unsplit and
@@ -688,7 +690,8 @@ AttendPlan plan_attend_wide(int64_t head_dim, int64_t heads_k, int64_t group, in
   AttendPlan p;
   p.head_dim = (int)head_dim;
   const int64_t rows = max_q * group;
-  p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 128 || head_dim != 128 ? 8 : 16;
+  const bool four = rows <= 128 || (rows > 256 && rows <= 384) || head_dim != 128;
+  p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : four ? 8 : 16;
   const int64_t tiles = (rows + 16 * p.row_tile - 1) / (16 * p.row_tile);
   const int64_t resident = 256 * (head_dim == 256 || p.row_tile == 16 ? 1 : head_dim == 64 && p.row_tile == 8 ? 3 : 2);
   p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);

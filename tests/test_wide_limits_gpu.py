@@ -195,3 +195,12 @@ def test_waves_of_several_tokens(d, T):
 
     for a, b in zip(run(T), run(300)):
         assert C.same_bits(a, b)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n_q", [25, 26, 51, 52, 64, 76, 77])
+def test_rows_around_whole_blocks(n_q, fmt):
+    """Blocks of 128 and 256 rows: 125 to 385 rows of a sequence."""
+    c = Case(fmt, n_q, 128, 10, 2, [700, n_q, 97], [n_q, n_q, 3], 32)
+    for causal, window in ((True, 0), (False, 0), (True, 50)):
+        c.check(c.run(causal=causal, window=window, max_q=n_q, max_len=700), causal=causal, window=window)
