@@ -682,18 +682,27 @@ AttendPlan plan_attend(int64_t head_dim, int64_t heads_k, int64_t group, int64_t
 // rows empty (4 x up to 64 rows x 5 heads on those tokens 78 us against 90; from 385
 // on eight are as fast or faster).
 //
-// A step of the latter takes 4.6 us, in which 18 MB of partial results go to memory
+// Up to 32 rows over a cache of rows are split for one block a compute unit, not the
+// two that it holds: its four waves keep enough loads in flight, and fewer splits are
+// joined (single tokens of 40 over 8 heads, 4 x 32768: 79.4 -> 68.4 us, 8 x 8192
+// 45.6 -> 41.4, 1 x 65536 54.1 -> 52.3, 16 x 1000 17.5 -> 15.4). From MXFP8, whose
+// loads are half as many bytes, 4 x 32768 would take 50.5 for 44.4. Workspaces are
+// sized for two.
+//
+// A step of the kernel for more rows takes 4.6 us, in which 18 MB of partial results go to memory
 // and back: 1024 rows x 5 heads on 4096 tokens, 160 blocks, are 123 us unsplit and
 // 144 in three parts.
-AttendPlan plan_attend_wide(int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t T, int64_t max_q,
-                            int64_t max_len, int64_t window) {
+AttendPlan plan_attend_wide(bool codes, int64_t head_dim, int64_t heads_k, int64_t group, int64_t B, int64_t T,
+                            int64_t max_q, int64_t max_len, int64_t window) {
   AttendPlan p;
   p.head_dim = (int)head_dim;
   const int64_t rows = max_q * group;
   const bool four = rows <= 128 || (rows > 256 && rows <= 384) || head_dim != 128;
   p.row_tile = rows <= 16 ? 1 : rows <= 32 ? 2 : four ? 8 : 16;
   const int64_t tiles = (rows + 16 * p.row_tile - 1) / (16 * p.row_tile);
-  const int64_t resident = 256 * (head_dim == 256 || p.row_tile == 16 ? 1 : head_dim == 64 && p.row_tile == 8 ? 3 : 2);
+  const int64_t resident = 256 * (head_dim == 256 || p.row_tile == 16 || (!codes && p.row_tile <= 2) ? 1
+                                : head_dim == 64 && p.row_tile == 8                               ? 3
+                                                                                                  : 2);
   p.row_tiles = (int)row_tiles_of(tiles, 16 * p.row_tile, heads_k, group, B, T, resident);
   p.max_q = max_q;
   split_cache(&p, B * heads_k * p.row_tiles, resident, group, max_len, window, T * heads_k * group * (head_dim + 2) * 8,
@@ -902,8 +911,9 @@ int attend(const char* fn, bool wide, const qknorm_operand_t* q, int64_t T, int 
   const int64_t max_len = batch->max_len < capacity ? batch->max_len : capacity;
   if (!attend_sizes_ok(T, heads_q, cache->heads, head_dim, batch->B, max_q, max_len))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
-  AttendPlan p = (wide ? plan_attend_wide : plan_attend)(head_dim, cache->heads, heads_q / cache->heads, batch->B, T,
-                                                         max_q, max_len, window);
+  const int64_t group = heads_q / cache->heads;
+  const AttendPlan p = wide ? plan_attend_wide(codes, head_dim, cache->heads, group, batch->B, T, max_q, max_len, window)
+                            : plan_attend(head_dim, cache->heads, group, batch->B, T, max_q, max_len, window);
   const int64_t block = wide && p.row_tile == 16 ? 512 : 256;
   if ((int64_t)batch->B * cache->heads * p.row_tiles > kLaunchThreads / block / p.splits)
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: the launch exceeds the grid", fn);
@@ -1059,7 +1069,7 @@ size_t qknorm_paged_attend_wide_workspace(int64_t T, int64_t heads_q, int64_t he
                                           int64_t max_q, int64_t max_len) {
   if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
   return attend_workspace(
-      plan_attend_wide(head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0), T, heads_q);
+      plan_attend_wide(true, head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0), T, heads_q);
 }
 
 }  // extern "C"
