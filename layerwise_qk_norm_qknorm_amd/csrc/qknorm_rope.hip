@@ -274,11 +274,13 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
     for (int e = 0; e < VW; ++e) ss = __builtin_fma((double)v[e], (double)v[e], ss);
     ss = group_sum_d(ss, L);
     // (head_dim is a power of two in this layout.) The hardware's estimate and two Newton
-    // steps instead of a division and a square root, which take 60 instructions more
+    // steps instead of a division and a square root, which take 60 instructions more. An
+    // estimate of 0 stays: m is infinite, where a step would make NaN of 0 m
     const double m = __builtin_fma(ss, (double)a.inv_div, (double)a.eps);
     r = __builtin_amdgcn_rsq(m);
+    const double finite = r > 0.0 ? m : 0.0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) r = __builtin_fma(r * 0.5, __builtin_fma(-m * r, r, 1.0), r);
+    for (int k = 0; k < 2; ++k) r = __builtin_fma(r * 0.5, __builtin_fma(-finite * r, r, 1.0), r);
   }
   bool in = false;
   const float* row = nullptr;
