@@ -427,7 +427,8 @@ int qknorm_paged_append_axes(const qknorm_operand_t* q, const qknorm_operand_t* 
  *           the last page, leaves its row as it was. The same slot may occur more than
  *           once.
  *   dtype   QKNORM_F32 or QKNORM_BF16: the type of the rows written. Codes are widened
- *           exactly where their value fits it (bf16: all values of at least 2^-133).
+ *           exactly where their value fits it (bf16: all values of at least 2^-130, and below
+ *           it multiples of 2^-133; others are rounded to nearest).
  *   k_rows, ld_k, v_rows, ld_v  row strides in elements, >= cache->heads * head_dim;
  *           one of them may be NULL (not wanted). They must not overlap each other or
  *           the cache.

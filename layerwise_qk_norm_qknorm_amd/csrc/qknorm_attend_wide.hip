@@ -5,7 +5,7 @@
 // out_r = sum_t softmax_t(scale q_r . k_t) v_t, in one pass over the cache:
 // a running maximum m and sum l per row, and an accumulator that is rescaled
 // when m grows. MXFP8 codes are widened to bf16 with their scale applied,
-// exactly (four significant bits times a power of two), so both products run on
+// exactly (four significant bits times a power of two, from 2^-130 on), so both products run on
 // bf16 MFMA tiles with nothing lost on the K and V side. Probabilities are
 // rounded to bf16, which the second product takes (at most half a step, 2^-8
 // relative, averaged over the tokens); scores, m, l and the accumulator are
@@ -67,7 +67,7 @@ struct Raw {              // 16 bytes of a token's head, and their scale
   uint32_t scale;
 };
 
-// Eight codes, two words, as bf16.
+// Eight codes, two words, as bf16. (The conversion takes the scale's exponent field: 0 is 2^-127.)
 __device__ __forceinline__ void widen8(const uint32_t* c, uint32_t scale_byte, uint32_t (&o)[4]) {
   const float s = __uint_as_float(scale_byte << 23);
   o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], s, false));
@@ -164,7 +164,7 @@ __device__ __forceinline__ float value_at(const AttendArgs& a, const Source& v, 
     const uint32_t scale =
         load_at<uint8_t>(v.scales + (uint32_t)id * (uint64_t)a.scale_page_stride + off * (uint64_t)a.scale_row, channel >> 5);
     if (scale > kTopScale8) return __builtin_nanf("");
-    return __builtin_amdgcn_cvt_f32_fp8(code, 0) * __uint_as_float(scale << 23);
+    return __builtin_amdgcn_cvt_f32_fp8(code, 0) * scale_value(scale);
   } else {
     return __uint_as_float((uint32_t)load_at<uint16_t>(row, 2 * channel) << 16);
   }

@@ -1,7 +1,7 @@
 // Reading a paged key / value cache back as rows, on gfx950 (CDNA4): token t's
 // keys and values, from the slot it names, as elements of the row type. Codes are
 // widened with their scale applied, exactly (a code has at most four significant
-// bits).
+// bits; bf16 holds those of values below 2^-130 only in part).
 //
 // It streams: bound by HBM. A lane takes 16 bytes of the rows written (one element
 // where they are not aligned), and a wave 64 of them of one token's K or V, so that

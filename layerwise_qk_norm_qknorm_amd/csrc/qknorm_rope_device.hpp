@@ -303,7 +303,7 @@ __device__ __forceinline__ Codes<MX, VW> codes_of(const float (&a)[VW]) {
 // The values that codes with a scale byte stand for (exact).
 template <class MX, int VW>
 __device__ __forceinline__ void code_values(const Codes<MX, VW>& q, int byte, float (&f)[VW]) {
-  const float back = __uint_as_float(byte == 0xFF ? 0x7FC00000u : (uint32_t)byte << 23);
+  const float back = byte == 0xFF ? __builtin_nanf("") : scale_value(byte);
   if constexpr (MX::kBits == 4) {
     const f32x2_t y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w[0], 1.0f, 0);
     const f32x2_t y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q.w[0], 1.0f, 1);
