@@ -717,6 +717,9 @@ bool attend_sizes_ok(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_d
          max_q <= kMaxTokens && max_len > 0 && max_len <= kMaxTokens;
 }
 
+// Query rows whose numbers, with all heads of a group side by side, keep clear of 32 bits.
+bool attend_rows_ok(int64_t T, int64_t group) { return T <= kMaxTokens / 4 / group; }
+
 size_t attend_workspace(const AttendPlan& p, int64_t T, int64_t heads_q) {
   if (p.most_splits <= 1) return 0;
   return (size_t)T * (size_t)heads_q * (size_t)p.most_splits * (size_t)(p.head_dim + 2) * 4;
@@ -912,6 +915,8 @@ int attend(const char* fn, bool wide, const qknorm_operand_t* q, int64_t T, int 
   if (!attend_sizes_ok(T, heads_q, cache->heads, head_dim, batch->B, max_q, max_len))
     return fail(QKNORM_ERR_UNSUPPORTED, "%s: sizes beyond the kernel's limits (65536 query heads, 2^20 sequences)", fn);
   const int64_t group = heads_q / cache->heads;
+  if (!attend_rows_ok(T, group))
+    return fail(QKNORM_ERR_UNSUPPORTED, "%s: T = %lld query rows are too many", fn, (long long)T);
   const AttendPlan p = wide ? plan_attend_wide(codes, head_dim, cache->heads, group, batch->B, T, max_q, max_len, window)
                             : plan_attend(head_dim, cache->heads, group, batch->B, T, max_q, max_len, window);
   const int64_t block = wide && p.row_tile == 16 ? 512 : 256;
@@ -920,9 +925,6 @@ int attend(const char* fn, bool wide, const qknorm_operand_t* q, int64_t T, int 
   const size_t need = attend_workspace(p, T, heads_q);
   if (need && (!workspace || !multiple(workspace, 16) || workspace_bytes < need))
     return fail(QKNORM_ERR_INVALID_ARG, "%s: the workspace must be 16-byte aligned, at least %zu bytes", fn, need);
-
-  if (T > kMaxTokens / 4 / (heads_q / cache->heads))
-    return fail(QKNORM_ERR_UNSUPPORTED, "%s: T = %lld query rows are too many", fn, (long long)T);
 
   const Region y{(uintptr_t)q->y, q->ld_y, q->h, T, 2};
   const Region ws = bytes_of(workspace, (int64_t)need);
@@ -1060,14 +1062,18 @@ int qknorm_paged_attend_wide(const qknorm_operand_t* q, int64_t T, int dtype, co
 
 size_t qknorm_paged_attend_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
                                      int64_t max_q, int64_t max_len) {
-  if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
+  if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0 ||
+      !attend_rows_ok(T, heads_q / heads_k))
+    return 0;
   return attend_workspace(plan_attend(head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0),
                           T, heads_q);
 }
 
 size_t qknorm_paged_attend_wide_workspace(int64_t T, int64_t heads_q, int64_t heads_k, int64_t head_dim, int64_t B,
                                           int64_t max_q, int64_t max_len) {
-  if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0) return 0;
+  if (!attend_sizes_ok(T, heads_q, heads_k, head_dim, B, max_q, max_len) || T == 0 || B == 0 ||
+      !attend_rows_ok(T, heads_q / heads_k))
+    return 0;
   return attend_workspace(
       plan_attend_wide(true, head_dim, heads_k, heads_q / heads_k, B, T, max_q < T ? max_q : T, max_len, 0), T, heads_q);
 }
