@@ -603,7 +603,8 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
   constexpr int KS = D / 16;                 // steps of the first product
   constexpr int kPer = D / F::kVW;           // lanes across a token
   constexpr int kAt = 64 / kPer;             // tokens of one wave's load
-  constexpr int PL = (kTok + NW * kAt - 1) / (NW * kAt);   // loads a thread makes of K, and of V
+  static_assert(kTok % (NW * kAt) == 0, "every wave loads the same share of a tile");
+  constexpr int PL = kTok / (NW * kAt);      // loads a thread makes of K, and of V
   constexpr int LDK = D * 2 + 16, LDV = D * 2 + 64;   // bytes of a row: no two of those read together share a bank
   constexpr int kBlock = 32 * NW;   // rows of a block
   constexpr int kTileK = kTok * LDK, kTileV = kTok * LDV;
@@ -630,7 +631,6 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
   const int heads_q = a.heads_k * a.group;
   const uint32_t off = (lane / kPer) * (uint32_t)a.token_stride + (lane % kPer) * 16;
   const uint32_t s_off = (lane / kPer) * (D / 32) + (lane % kPer) / 2;
-  const bool loads = NW * kAt <= kTok || wave * kAt < kTok;      // a tile of 64 MXFP8 columns is less than eight waves load at a time
 
   for (int b0 = grid_tile * kBlock; b0 < rows; b0 += a.row_tiles * kBlock) {
     const int i_first = over(b0, a.by_group);
@@ -686,7 +686,6 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
       int ids = pages_from(begin), ids_from = begin, ids_next = pages_from(begin + 1024);
       // this wave's share of a tile: tokens (x * NW + wave) * kAt and on
       const auto load = [&](int tok) {
-        if (!loads) return;
         if (tok >= ids_from + 1024) {
           ids_from += 1024;
           ids = ids_next;
@@ -711,7 +710,6 @@ __global__ void __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) qknor
       };
       const int put_k = lane / kPer * LDK + lane % kPer * (F::kVW * 2), put_v = lane / kPer * LDV + lane % kPer * (F::kVW * 2);
       const auto store = [&](int tok, int buf) {
-        if (!loads) return;
         const bool edge = tok < block_lo || tok + kTok > min(block_hi, end);
         uint32_t top = 0;
         if constexpr (F::kCodes) {
