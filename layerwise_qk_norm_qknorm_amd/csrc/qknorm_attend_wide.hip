@@ -152,7 +152,7 @@ __device__ __forceinline__ int page_of(const AttendArgs& a, const int32_t* table
 }
 
 // Element (token, channel) of V as float32. For the few tiles with infinities or NaN
-// next to a mask.
+// next to a mask: what matters is whether it is one of them (the scale byte 0 may be 0 here).
 template <class F>
 __device__ __forceinline__ float value_at(const AttendArgs& a, const Source& v, const int32_t* table, int t, int channel) {
   const int id = load_uniform(table + (t >> a.log2_page));
@@ -164,7 +164,7 @@ __device__ __forceinline__ float value_at(const AttendArgs& a, const Source& v, 
     const uint32_t scale =
         load_at<uint8_t>(v.scales + (uint32_t)id * (uint64_t)a.scale_page_stride + off * (uint64_t)a.scale_row, channel >> 5);
     if (scale > kTopScale8) return __builtin_nanf("");
-    return __builtin_amdgcn_cvt_f32_fp8(code, 0) * scale_value(scale);
+    return __builtin_amdgcn_cvt_f32_fp8(code, 0) * __uint_as_float(scale << 23);
   } else {
     return __uint_as_float((uint32_t)load_at<uint16_t>(row, 2 * channel) << 16);
   }

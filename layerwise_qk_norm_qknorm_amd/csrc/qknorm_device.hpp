@@ -393,10 +393,6 @@ __device__ __forceinline__ T load_uniform(const T* p) {
   return *reinterpret_cast<cptr>(reinterpret_cast<uintptr_t>(p));
 }
 
-// What a block's scale byte stands for: 2^(byte - 127), for bytes up to 254. The exponent
-// field of 0 is subnormal: 2^-127 has the bits 0x00400000.
-__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
-
 // A block-uniform 64-bit value, held in scalar registers: lanes that select
 // between two such values then need no vector arithmetic to form them.
 __device__ __forceinline__ uint64_t uniform64(uint64_t v) {

@@ -300,6 +300,9 @@ __device__ __forceinline__ Codes<MX, VW> codes_of(const float (&a)[VW]) {
   }
   return q;
 }
+// What a block's scale byte stands for: 2^(byte - 127), for bytes up to 254. The exponent
+// field of 0 is subnormal: 2^-127 has the bits 0x00400000.
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
 // The values that codes with a scale byte stand for (exact).
 template <class MX, int VW>
 __device__ __forceinline__ void code_values(const Codes<MX, VW>& q, int byte, float (&f)[VW]) {
