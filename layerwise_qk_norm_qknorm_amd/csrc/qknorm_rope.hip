@@ -346,7 +346,7 @@ __device__ __forceinline__ void exact_chunk(const RopeArgs& a, const char* x, co
 // its slots.
 // 8192 tokens of 40 + 8 + 8 bf16 heads of 128 into a 4-bit cache: 60.4 us, 4.1
 // TB/s, 58.1 without the cached values as rows; Q's launch 33 us runs at 5.1
-// TB/s, K's and V's 27 us issues 504 vector instructions a wave in 65% of the
+// TB/s, K's and V's 27 us issues 449 vector instructions a wave in 60% of the
 // cycles, beside 81 MB of traffic. Into a cache of bf16 rows 42.0 us, 5.7 TB/s. Into an
 // 8-bit cache, on three axes, 67.2: Q's launch 37 us, K's and V's 30 (566 vector
 // instructions a wave, 15 us of issue, 63% of the busy cycles; 87 MB, 14 us).
